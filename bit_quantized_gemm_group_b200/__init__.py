@@ -22,15 +22,19 @@ STATUS = {0: "QG_OK", 1: "QG_ERR_NULL", 2: "QG_ERR_SHAPE", 3: "QG_ERR_ALIGN", 4:
 QG_OK, QG_ERR_NULL, QG_ERR_SHAPE, QG_ERR_ALIGN, QG_ERR_DTYPE = 0, 1, 2, 3, 4
 QG_ERR_NONFINITE, QG_ERR_RANGE, QG_ERR_TIMEOUT, QG_ERR_CUDA, QG_ERR_UNSUPPORTED = 5, 6, 7, 8, 9
 QG_ERR_WORKSPACE = 10
-QG_F16, QG_BF16 = 0, 1
+QG_F16, QG_BF16, QG_F32 = 0, 1, 2
 QG_OP_GEMM_W4A16, QG_OP_GEMM_W8A8, QG_OP_GEMM_W4A8, QG_OP_AWQ_SEARCH, QG_OP_GPTQ = 0, 1, 2, 3, 4
+QG_OP_GEMM_FP8, QG_OP_GEMM_FP8_EXPERTS, QG_OP_EXPERT_SLOTS = 5, 6, 7
+QG_SCORE_SOFTMAX, QG_SCORE_SIGMOID = 0, 1
 
 EXPORTS = ["qg_quantize_w4_group", "qg_pack_nibbles", "qg_gemm_w4a16", "qg_smooth_quant_act_i8", "qg_gemm_w8a8",
            "qg_gemm_w4a8", "qg_smooth_scales", "qg_quantize_w8_channel", "qg_device_status", "qg_status_string",
            "qg_last_error", "qg_selftest_bounded_wait", "qg_workspace_size", "qg_gemm_w4a16_noalloc",
            "qg_awq_act_mean", "qg_awq_scales", "qg_awq_scale_act", "qg_awq_search", "qg_outlier_split_w4",
            "qg_outlier_side_add", "qg_gemm_w4a16_outlier", "qg_prune24", "qg_pack24_vals", "qg_gemm_w4a16_24",
-           "qg_gptq", "qg_gptq_blocked", "qg_pack24_tc", "qg_gemm_w4a16_24_tc"]
+           "qg_gptq", "qg_gptq_blocked", "qg_pack24_tc", "qg_gemm_w4a16_24_tc", "qg_quantize_act_fp8",
+           "qg_quantize_weight_fp8", "qg_gemm_fp8", "qg_route_topk", "qg_expert_slots", "qg_gemm_fp8_experts",
+           "qg_combine_experts"]
 
 
 class QgError(RuntimeError):
@@ -67,6 +71,13 @@ _SIGS = {
     "qg_awq_scales": [_P, _I, ctypes.c_double, _P, _P, _P],
     "qg_awq_scale_act": [_P, _I, _I, _P, _P, _P],
     "qg_awq_search": [_P, _I, _I, _P, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P],
+    "qg_quantize_act_fp8": [_P, _I, _I, _I, _P, _P, _P],
+    "qg_quantize_weight_fp8": [_P, _I, _I, _I, _I, _P, _P, _P],
+    "qg_gemm_fp8": [_P, _P, _I, _I, _P, _P, _I, _P, _I, _P, _SZ, _P],
+    "qg_route_topk": [_P, _I, _I, _I, _P, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P],
+    "qg_expert_slots": [_P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P],
+    "qg_gemm_fp8_experts": [_P, _P, _I, _I, _P, _P, _I, _I, _P, _P, _I, _P, _I, _P, _SZ, _P],
+    "qg_combine_experts": [_P, _I, _I, _I, _P, _P, _I, _I, _P, _P],
     "qg_device_status": [_P],
     "qg_selftest_bounded_wait": [ctypes.c_uint64, _P],
 }
@@ -310,6 +321,165 @@ def qg_awq_search(Xcal, W, n_grid, mse, best, s, inv_s, group=128, workspace="au
     wp, wb = _ws(workspace, QG_OP_AWQ_SEARCH, Mc, K, N, Xcal.device)
     _check(lib().qg_awq_search(_ptr(Xcal), Mc, K, _ptr(W), N, group, n_grid, _ptr(mse), _ptr(best), _ptr(s),
                               _ptr(inv_s), wp, wb, _stream(stream)), "qg_awq_search")
+
+
+# ---------------------------------------------------------------------------
+# The FP8 layer and its experts.  These calls check types and shapes here (a wrong
+# shape would read past a buffer), run on the device of their tensors and, with
+# workspace="auto", take their scratch from torch's allocator for the one call: calls on
+# several streams and captured graphs then share none.
+# ---------------------------------------------------------------------------
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_HALF = {torch.float16: QG_F16, torch.bfloat16: QG_BF16}
+_FLOAT = {torch.float16: QG_F16, torch.bfloat16: QG_BF16, torch.float32: QG_F32}
+_SCORES = {"softmax": QG_SCORE_SOFTMAX, "sigmoid": QG_SCORE_SIGMOID}
+
+
+def _want(where, name, t, types, shape, device):
+    if t.dtype not in types:
+        raise ValueError(f"{where}: {name} has dtype {t.dtype}, not one of {', '.join(map(str, types))}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, not {shape}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{where}: {name} is on {t.device}: all tensors have to be on one GPU ({device})")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} has to be contiguous (row-major)")
+
+
+def _rank(where, name, t, n):
+    if t.dim() != n:
+        raise ValueError(f"{where}: {name} has {t.dim()} dimensions, not {n}")
+
+
+def _cdiv(a, b):
+    return -(-a // b)
+
+
+def _run(where, device, stream, args, op=None, workspace=None):
+    """Calls `where` with `args`, then (op = (op, M, K, N)) the workspace, then the stream, on `device`."""
+    with torch.cuda.device(device):
+        st = torch.cuda.current_stream(device) if stream is None else stream
+        if op is not None:
+            need = lib().qg_workspace_size(*op)
+            if isinstance(workspace, str) and workspace == "auto":
+                workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+                if workspace is not None and stream is not None:
+                    workspace.record_stream(stream)
+            if workspace is None or workspace is False:
+                args += (None, 0)
+            else:
+                _want(where, "workspace", workspace, (torch.uint8,), (workspace.numel(),), device)
+                args += (workspace.data_ptr(), workspace.numel())
+        _check(getattr(lib(), where)(*args, st.cuda_stream), where)
+
+
+def qg_quantize_act_fp8(X, Xq, xs, stream=None):
+    """X fp16 or bf16 [M, K] -> Xq e4m3 [M, K] and xs fp32 [M, ceil(K / 128)]."""
+    f = "qg_quantize_act_fp8"
+    _rank(f, "X", X, 2)
+    M, K = X.shape
+    _want(f, "X", X, _HALF, (M, K), X.device)
+    _want(f, "Xq", Xq, _E4M3, (M, K), X.device)
+    _want(f, "xs", xs, (torch.float32,), (M, _cdiv(K, 128)), X.device)
+    _run(f, X.device, stream, (X.data_ptr(), _HALF[X.dtype], M, K, Xq.data_ptr(), xs.data_ptr()))
+
+
+def qg_quantize_weight_fp8(W, Wq, ws, stream=None):
+    """W fp32, bf16 or fp16 [K, N] (or [E, K, N]) -> Wq e4m3 of that shape and ws fp32
+    [ceil(K / 128), ceil(N / 128)] (or [E, ..])."""
+    f = "qg_quantize_weight_fp8"
+    _rank(f, "W", W, 2 if W.dim() == 2 else 3)
+    K, N = W.shape[-2:]
+    _want(f, "W", W, _FLOAT, tuple(W.shape), W.device)
+    _want(f, "Wq", Wq, _E4M3, tuple(W.shape), W.device)
+    _want(f, "ws", ws, (torch.float32,), (*W.shape[:-2], _cdiv(K, 128), _cdiv(N, 128)), W.device)
+    E = W.shape[0] if W.dim() == 3 else 1
+    _run(f, W.device, stream, (W.data_ptr(), _FLOAT[W.dtype], E, K, N, Wq.data_ptr(), ws.data_ptr()))
+
+
+def qg_gemm_fp8(Xq, xs, Wq, ws, Y, workspace="auto", stream=None):
+    """Y [M, N] (fp16 or bf16) = X W of Xq [M, K], xs, Wq [K, N], ws (the quantizers' layouts)."""
+    f = "qg_gemm_fp8"
+    _rank(f, "Xq", Xq, 2)
+    _rank(f, "Wq", Wq, 2)
+    (M, K), N, dev = Xq.shape, Wq.shape[1], Xq.device
+    G = _cdiv(K, 128)
+    _want(f, "Xq", Xq, _E4M3, (M, K), dev)
+    _want(f, "xs", xs, (torch.float32,), (M, G), dev)
+    _want(f, "Wq", Wq, _E4M3, (K, N), dev)
+    _want(f, "ws", ws, (torch.float32,), (G, _cdiv(N, 128)), dev)
+    _want(f, "Y", Y, _HALF, (M, N), dev)
+    _run(f, dev, stream, (Xq.data_ptr(), xs.data_ptr(), M, K, Wq.data_ptr(), ws.data_ptr(), N, Y.data_ptr(),
+                          _HALF[Y.dtype]), (QG_OP_GEMM_FP8, M, K, N), workspace)
+
+
+def qg_route_topk(logits, bias, idx, weights, score="softmax", n_group=1, topk_group=1, group_top=1, renorm=True,
+                  scale=1.0, stream=None):
+    """logits [M, E] (and bias fp32 [E] or None) -> idx int32 [M, topk], weights fp32 [M, topk]."""
+    f = "qg_route_topk"
+    if score not in _SCORES:
+        raise ValueError(f"{f}: score is {score!r}, not one of {', '.join(_SCORES)}")
+    _rank(f, "logits", logits, 2)
+    _rank(f, "idx", idx, 2)
+    (M, E), topk, dev = logits.shape, idx.shape[1], logits.device
+    _want(f, "logits", logits, _FLOAT, (M, E), dev)
+    if bias is not None:
+        _want(f, "bias", bias, (torch.float32,), (E,), dev)
+    _want(f, "idx", idx, (torch.int32,), (M, topk), dev)
+    _want(f, "weights", weights, (torch.float32,), (M, topk), dev)
+    _run(f, dev, stream, (logits.data_ptr(), _FLOAT[logits.dtype], M, E, None if bias is None else bias.data_ptr(),
+                          _SCORES[score], n_group, topk_group, group_top, topk, int(bool(renorm)), scale,
+                          idx.data_ptr(), weights.data_ptr()))
+
+
+def qg_expert_slots(idx, offsets, slot_token, token_slot, workspace="auto", stream=None):
+    """idx int32 [M, topk] -> offsets int32 [E + 1], slot_token int32 [M * topk], token_slot int32 [M, topk]."""
+    f = "qg_expert_slots"
+    _rank(f, "idx", idx, 2)
+    _rank(f, "offsets", offsets, 1)
+    (M, topk), E, dev = idx.shape, offsets.shape[0] - 1, idx.device
+    _want(f, "idx", idx, (torch.int32,), (M, topk), dev)
+    _want(f, "offsets", offsets, (torch.int32,), (E + 1,), dev)
+    _want(f, "slot_token", slot_token, (torch.int32,), (M * topk,), dev)
+    _want(f, "token_slot", token_slot, (torch.int32,), (M, topk), dev)
+    _run(f, dev, stream, (idx.data_ptr(), M, topk, E, offsets.data_ptr(), slot_token.data_ptr(),
+                          token_slot.data_ptr()), (QG_OP_EXPERT_SLOTS, M, topk, E), workspace)
+
+
+def qg_gemm_fp8_experts(Xq, xs, slot_token, offsets, Wq, ws, Y, workspace="auto", stream=None):
+    """Y [S, N]: the rows offsets[e] .. offsets[e + 1] - 1 are the rows slot_token[s] of X (slot_token None:
+    rows s) times the expert weight Wq[e] [K, N]; the rows of Y from offsets[E] on are left as they were."""
+    f = "qg_gemm_fp8_experts"
+    _rank(f, "Xq", Xq, 2)
+    _rank(f, "Wq", Wq, 3)
+    _rank(f, "Y", Y, 2)
+    (Mx, K), (E, _, N), S, dev = Xq.shape, Wq.shape, Y.shape[0], Xq.device
+    G = _cdiv(K, 128)
+    _want(f, "Xq", Xq, _E4M3, (Mx, K), dev)
+    _want(f, "xs", xs, (torch.float32,), (Mx, G), dev)
+    if slot_token is not None:
+        _want(f, "slot_token", slot_token, (torch.int32,), (S,), dev)
+    _want(f, "offsets", offsets, (torch.int32,), (E + 1,), dev)
+    _want(f, "Wq", Wq, _E4M3, (E, K, N), dev)
+    _want(f, "ws", ws, (torch.float32,), (E, G, _cdiv(N, 128)), dev)
+    _want(f, "Y", Y, _HALF, (S, N), dev)
+    _run(f, dev, stream, (Xq.data_ptr(), xs.data_ptr(), Mx, K, None if slot_token is None else slot_token.data_ptr(),
+                          offsets.data_ptr(), S, E, Wq.data_ptr(), ws.data_ptr(), N, Y.data_ptr(), _HALF[Y.dtype]),
+         (QG_OP_GEMM_FP8_EXPERTS, S, K, N), workspace)
+
+
+def qg_combine_experts(D, token_slot, weights, Y, stream=None):
+    """Y [M, N] = the sum over j of weights[m, j] D[token_slot[m, j]] (D fp16 or bf16 [S, N]; slot -1 adds nothing)."""
+    f = "qg_combine_experts"
+    _rank(f, "D", D, 2)
+    _rank(f, "token_slot", token_slot, 2)
+    (S, N), (M, topk), dev = D.shape, token_slot.shape, D.device
+    _want(f, "D", D, _HALF, (S, N), dev)
+    _want(f, "token_slot", token_slot, (torch.int32,), (M, topk), dev)
+    _want(f, "weights", weights, (torch.float32,), (M, topk), dev)
+    _want(f, "Y", Y, (D.dtype,), (M, N), dev)
+    _run(f, dev, stream, (D.data_ptr(), _HALF[D.dtype], S, N, token_slot.data_ptr(), weights.data_ptr(), M, topk,
+                          Y.data_ptr()))
 
 
 def qg_device_status(stream=None) -> int:

@@ -28,6 +28,9 @@
 #include "int8_decode.cuh"
 #include "w4a8_decode.cuh"
 #include "w4a16_skinny.cuh"
+#include "fp8_quant.cuh"
+#include "fp8_gemm.cuh"
+#include "moe.cuh"
 
 namespace {
 
@@ -863,6 +866,8 @@ qg_status launch_w4a8_skinny(const qg::Int8SkinnyParams& p, qg_stream_t stream)
 
 }  // namespace
 
+#include "fp8_host.cuh"
+
 // ===========================================================================
 // C ABI
 // ===========================================================================
@@ -894,6 +899,9 @@ size_t qg_workspace_size(qg_op op, int M, int K, int N)
         if (M < 1 || K < 8 || K % 8 || K > 16384 || N < 1) return 0;
         return std::max(gptq_carve(nullptr, K, N).bytes, gptq_blocked_carve(nullptr, M, K, N).bytes);
     }
+    if (op == QG_OP_GEMM_FP8) return M < 1 || fp8_bad_shape(K, N) ? 0 : fp8_workspace(M, K, N, false);
+    if (op == QG_OP_GEMM_FP8_EXPERTS) return M < 1 || fp8_bad_shape(K, N) ? 0 : fp8_workspace(M, K, N, true);
+    if (op == QG_OP_EXPERT_SLOTS) return M < 1 || slots_bad_shape(M, K, N) ? 0 : slots_workspace(M, K, N);
     if (M < 1 || K < 128 || N < 8 || K % 128) return 0;
     switch (op) {
         case QG_OP_GEMM_W4A16: {
@@ -1522,6 +1530,93 @@ qg_status qg_quantize_w8_channel(const float* W, const float* s, int K, int N, i
                                                                                                           Wq, sw);
     QG_CUDA(cudaGetLastError());
     return QG_OK;
+}
+
+qg_status qg_quantize_act_fp8(const void* X, qg_dtype xdt, int M, int K, uint8_t* Xq, float* xs, qg_stream_t stream)
+{
+    if (xdt != QG_F16 && xdt != QG_BF16) return QG_ERR_DTYPE;
+    if (M < 0 || K < 16 || K % 16) return QG_ERR_SHAPE;
+    if (M == 0) return QG_OK;
+    if (!X || !Xq || !xs) return QG_ERR_NULL;
+    if (misaligned(X) || misaligned(Xq) || misaligned(xs)) return QG_ERR_ALIGN;
+    return xdt == QG_BF16 ? quantize_act_fp8<qg::IN_BF16>(X, M, K, Xq, xs, stream)
+                          : quantize_act_fp8<qg::IN_F16>(X, M, K, Xq, xs, stream);
+}
+
+qg_status qg_quantize_weight_fp8(const void* W, qg_dtype wdt, int E, int K, int N, uint8_t* Wq, float* ws,
+                                 qg_stream_t stream)
+{
+    if (wdt != QG_F16 && wdt != QG_BF16 && wdt != QG_F32) return QG_ERR_DTYPE;
+    if (E < 1 || fp8_bad_shape(K, N) || E > 65535 || (K + 127) / 128 > 65535) return QG_ERR_SHAPE;
+    if (!W || !Wq || !ws) return QG_ERR_NULL;
+    if (misaligned(W) || misaligned(Wq) || misaligned(ws)) return QG_ERR_ALIGN;
+    return wdt == QG_F32    ? quantize_weight_fp8<qg::IN_F32>(W, E, K, N, Wq, ws, stream)
+           : wdt == QG_BF16 ? quantize_weight_fp8<qg::IN_BF16>(W, E, K, N, Wq, ws, stream)
+                            : quantize_weight_fp8<qg::IN_F16>(W, E, K, N, Wq, ws, stream);
+}
+
+qg_status qg_gemm_fp8(const uint8_t* Xq, const float* xs, int M, int K, const uint8_t* Wq, const float* ws, int N,
+                      void* Y, qg_dtype ydt, void* workspace, size_t ws_bytes, qg_stream_t stream)
+{
+    if (ydt != QG_F16 && ydt != QG_BF16) return QG_ERR_DTYPE;
+    if (M < 0 || fp8_bad_shape(K, N)) return QG_ERR_SHAPE;
+    if (M == 0) return QG_OK;
+    return fp8_gemm(Xq, xs, M, K, nullptr, nullptr, M, 1, Wq, ws, N, Y, ydt, workspace, ws_bytes, stream);
+}
+
+qg_status qg_gemm_fp8_experts(const uint8_t* Xq, const float* xs, int Mx, int K, const int32_t* slot_token,
+                              const int32_t* offsets, int S, int E, const uint8_t* Wq, const float* ws, int N, void* Y,
+                              qg_dtype ydt, void* workspace, size_t ws_bytes, qg_stream_t stream)
+{
+    if (ydt != QG_F16 && ydt != QG_BF16) return QG_ERR_DTYPE;
+    if (S < 0 || Mx < 0 || fp8_bad_shape(K, N) || E < 1 || E > qg::kMaxExperts) return QG_ERR_SHAPE;
+    if (S == 0) return QG_OK;
+    if (Mx < 1 || (!slot_token && Mx < S)) return QG_ERR_SHAPE;
+    if (!offsets) return QG_ERR_NULL;
+    return fp8_gemm(Xq, xs, Mx, K, slot_token, offsets, S, E, Wq, ws, N, Y, ydt, workspace, ws_bytes, stream);
+}
+
+qg_status qg_route_topk(const void* logits, qg_dtype ldt, int M, int E, const float* bias, qg_score score, int n_group,
+                        int topk_group, int group_top, int topk, int renorm, float scale, int32_t* idx, float* weights,
+                        qg_stream_t stream)
+{
+    if ((ldt != QG_F16 && ldt != QG_BF16 && ldt != QG_F32) || (score != QG_SCORE_SOFTMAX && score != QG_SCORE_SIGMOID))
+        return QG_ERR_DTYPE;
+    if (M < 0 || E < 1 || E > qg::kMaxExperts || topk < 1 || topk > std::min(E, qg::kMaxTopk) || n_group < 1 ||
+        n_group > qg::kMaxExpertGroups || E % n_group || topk_group < 1 || topk_group > n_group || group_top < 1 ||
+        group_top > 2 || topk > topk_group * (E / n_group))
+        return QG_ERR_SHAPE;
+    if (M == 0) return QG_OK;
+    if (!logits || !idx || !weights) return QG_ERR_NULL;
+    if (misaligned(logits) || misaligned(bias) || misaligned(idx) || misaligned(weights)) return QG_ERR_ALIGN;
+    const qg::RouteParams p{logits, bias,       idx,        weights,   M,
+                            E,      topk,       n_group,    topk_group, group_top,
+                            score == QG_SCORE_SIGMOID, renorm != 0, scale};
+    return ldt == QG_F32    ? route_topk<qg::IN_F32>(p, stream)
+           : ldt == QG_BF16 ? route_topk<qg::IN_BF16>(p, stream)
+                            : route_topk<qg::IN_F16>(p, stream);
+}
+
+qg_status qg_expert_slots(const int32_t* idx, int M, int topk, int E, int32_t* offsets, int32_t* slot_token,
+                          int32_t* token_slot, void* workspace, size_t ws_bytes, qg_stream_t stream)
+{
+    if (slots_bad_shape(M, topk, E)) return QG_ERR_SHAPE;
+    if (!offsets || (M > 0 && (!idx || !slot_token || !token_slot))) return QG_ERR_NULL;
+    if (misaligned(idx) || misaligned(offsets) || misaligned(slot_token) || misaligned(token_slot) ||
+        misaligned(workspace))
+        return QG_ERR_ALIGN;
+    return expert_slots(idx, M, topk, E, offsets, slot_token, token_slot, workspace, ws_bytes, stream);
+}
+
+qg_status qg_combine_experts(const void* D, qg_dtype dt, int S, int N, const int32_t* token_slot, const float* weights,
+                             int M, int topk, void* Y, qg_stream_t stream)
+{
+    if (dt != QG_F16 && dt != QG_BF16) return QG_ERR_DTYPE;
+    if (M < 0 || S < 0 || N < 8 || N % 8 || topk < 1) return QG_ERR_SHAPE;
+    if (M == 0) return QG_OK;
+    if ((S > 0 && !D) || !token_slot || !weights || !Y) return QG_ERR_NULL;
+    if (misaligned(D) || misaligned(token_slot) || misaligned(weights) || misaligned(Y)) return QG_ERR_ALIGN;
+    return combine_experts(D, dt, S, N, token_slot, weights, M, topk, Y, stream);
 }
 
 qg_status qg_selftest_bounded_wait(uint64_t limit_ns, qg_stream_t stream)

@@ -16,6 +16,8 @@
  *        (hustzhy.cn), sec. 2.1-2.3 (AWQ): per-input-channel scales
  *        s_c = mean(|X_c|)^alpha, X W = (X / s)(s W), alpha chosen on a grid in
  *        [0, 1] by the least MSE of the quantized layer's output.
+ *   FP8: [Q] sec. 5 (e4m3), with the granularity of [Q] sec. 1.3 and [G] sec. 2.2 (groups
+ *        of 128); the router and the experts' calls around it state their own definition.
  *
  * Readings taken where the pages are silent (the same ones the test oracle takes):
  *   asymmetric INT4 uses s = (max' - min')/15 over a range widened to contain 0,
@@ -76,10 +78,17 @@ typedef enum {
     QG_OP_GEMM_W8A8 = 1,
     QG_OP_GEMM_W4A8 = 2,
     QG_OP_AWQ_SEARCH = 3,
-    QG_OP_GPTQ = 4
+    QG_OP_GPTQ = 4,
+    QG_OP_GEMM_FP8 = 5,
+    QG_OP_GEMM_FP8_EXPERTS = 6,
+    QG_OP_EXPERT_SLOTS = 7
 } qg_op;
 
-typedef enum { QG_F16 = 0, QG_BF16 = 1 } qg_dtype;
+/* QG_F32 only where a call lists it. */
+typedef enum { QG_F16 = 0, QG_BF16 = 1, QG_F32 = 2 } qg_dtype;
+
+/* How qg_route_topk scores the experts. */
+typedef enum { QG_SCORE_SOFTMAX = 0, QG_SCORE_SIGMOID = 1 } qg_score;
 
 /* --------------------------------------------------------------------------
  * Group-wise INT4 weight quantization.   [Q] sec. 1.1-1.3, [G] sec. 2.2
@@ -433,9 +442,110 @@ qg_status qg_awq_search(const uint16_t* Xcal, int Mc, int K, const float* W, int
                         int n_grid, double* mse, int32_t* best, float* s, float* inv_s,
                         void* workspace, size_t ws_bytes, qg_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * FP8 (e4m3) operands with a scale for each 128 of K.   [Q] sec. 1.1-1.3, sec. 5 (e4m3)
+ *
+ *   s = max|x| / 448 (fp32);  code = e4m3( fp32(x / s) ), both to nearest even
+ *   (448 is the largest e4m3 number);  s == 0 -> codes 0.
+ * Activations: one scale for each row and group of 128 columns; weights: one for each
+ *   block of 128 x 128.  With G = ceil(K / 128) and NB = ceil(N / 128) (the last group,
+ *   block row and block column may be short):
+ *   X fp16 or bf16 [M][K]; Xq e4m3 [M][K]; xs fp32 [M][G].
+ *   W fp16, bf16 or fp32 [E][K][N] (E = 1 for a plain layer); Wq e4m3 [E][K][N];
+ *   ws fp32 [E][G][NB].
+ * A group with a NaN or an infinity gets the scale NaN and codes 0 (its products are NaN,
+ *   as the unquantized ones would be) and sets QG_ERR_NONFINITE.
+ * Rules: K % 16 == 0; weights: N % 16 == 0, E >= 1 (K / 128 and E below 65536).
+ * ------------------------------------------------------------------------ */
+qg_status qg_quantize_act_fp8(const void* X, qg_dtype xdt, int M, int K, uint8_t* Xq, float* xs,
+                              qg_stream_t stream);
+qg_status qg_quantize_weight_fp8(const void* W, qg_dtype wdt, int E, int K, int N, uint8_t* Wq,
+                                 float* ws, qg_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * FP8 GEMM with block scales (W8A8 in e4m3).   [Q] sec. 1.3, sec. 5
+ *
+ *   P[m][g][n] = sum_{k in group g} Xq[m][k] * Wq[k][n]           (fp32)
+ *   Y[m][n]    = rn( sum_g (xs[m][g] * ws[g][n / 128]) * P[m][g][n] )   (fp32, one rounding)
+ *
+ * Xq e4m3 [M][K], xs fp32 [M][G], Wq e4m3 [K][N], ws fp32 [G][NB] as above; any fp32
+ * scales are taken, not only the quantizers'.  Y fp16 or bf16 [M][N] (ydt).
+ * NaN codes and scales give NaN in the rows and columns that read them, and there only.
+ * Rules: K % 16 == 0, N % 16 == 0.
+ * workspace: required when qg_workspace_size(QG_OP_GEMM_FP8, M, K, N) is not 0, and then
+ *   at least that many bytes (NULL -> QG_ERR_NULL, smaller -> QG_ERR_WORKSPACE); contents
+ *   irrelevant.  Calls that may run concurrently need workspaces of their own.
+ * ------------------------------------------------------------------------ */
+qg_status qg_gemm_fp8(const uint8_t* Xq, const float* xs, int M, int K, const uint8_t* Wq,
+                      const float* ws, int N, void* Y, qg_dtype ydt, void* workspace,
+                      size_t ws_bytes, qg_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Routing tokens to experts (a mixture of experts whose experts are quantized layers).
+ * The pages have no counterpart; the definition is:
+ *
+ *   score[m][e] = softmax over e of logits[m], or sigmoid(logits[m][e])
+ *   key[m][e]   = score[m][e] + bias[e]         (bias NULL: the score; it only selects)
+ *   n_group > 1: the experts form n_group groups of E / n_group; a group's value is the sum
+ *     of its group_top (1 or 2) largest keys, and only the topk_group groups of the largest
+ *     values stay
+ *   idx[m]      = the topk experts of the largest keys, largest first
+ *   weights[m]  = their scores; renorm: divided by their sum (0 if that is 0); times scale
+ *   Equal values: the lower index first, everywhere.  Scores, keys and sums are compared as
+ *   binary64 values; weights are rounded once to fp32.
+ * An expert whose logit or bias is -inf is not available to the token; a choice for which no
+ *   expert is left is idx -1 with weight 0 (a token of -inf logits goes to no expert).  A token
+ *   with a NaN or +inf logit or key goes to no expert and sets QG_ERR_NONFINITE.
+ * logits fp16, bf16 or fp32 [M][E] (ldt); bias fp32 [E] or NULL; idx int32 [M][topk];
+ * weights fp32 [M][topk].
+ * Rules: 1 <= E <= 512, 1 <= topk <= min(32, E), 1 <= n_group <= 32, E % n_group == 0,
+ *   1 <= topk_group <= n_group, group_top 1 or 2, topk <= topk_group * (E / n_group).
+ * ------------------------------------------------------------------------ */
+qg_status qg_route_topk(const void* logits, qg_dtype ldt, int M, int E, const float* bias,
+                        qg_score score, int n_group, int topk_group, int group_top, int topk,
+                        int renorm, float scale, int32_t* idx, float* weights, qg_stream_t stream);
+
+/* The slots of the experts' products: the choices sorted by expert, then by token (and by
+ * place within a token).
+ *   offsets[e] .. offsets[e + 1] - 1   the slots of expert e; offsets[E] the slots in use
+ *   slot_token[s]                      the token of slot s; -1 from offsets[E] on
+ *   token_slot[m][j]                   the slot of token m's choice j; -1 where idx is -1
+ * idx int32 [M][topk] (any routing's; an entry outside -1 .. E-1 counts as -1 and sets
+ * QG_ERR_RANGE); offsets int32 [E + 1]; slot_token int32 [M * topk]; token_slot int32
+ * [M][topk].  Rules: 1 <= E <= 512, topk >= 1, M * topk < 2^31; M == 0 sets the offsets to 0.
+ * workspace: as for qg_gemm_fp8, of qg_workspace_size(QG_OP_EXPERT_SLOTS, M, topk, E) bytes. */
+qg_status qg_expert_slots(const int32_t* idx, int M, int topk, int E, int32_t* offsets,
+                          int32_t* slot_token, int32_t* token_slot, void* workspace,
+                          size_t ws_bytes, qg_stream_t stream);
+
+/* The experts' products: for each expert e and its slots s = offsets[e] .. offsets[e + 1] - 1
+ *   Y[s] = row slot_token[s] of X (slot_token NULL: row s) times expert e's weight,
+ * each as qg_gemm_fp8.  Rows of Y from offsets[E] on are left as they were.
+ * Xq e4m3 [Mx][K], xs fp32 [Mx][G]; slot_token int32 [S] or NULL (then Mx >= S);
+ * offsets int32 [E + 1], ascending from 0 to at most S; Wq e4m3 [E][K][N], ws fp32
+ * [E][G][NB]; Y fp16 or bf16 [S][N].
+ * Device error: QG_ERR_RANGE -- offsets that are not ascending within 0 .. S (nothing is
+ *   computed), or a slot_token outside 0 .. Mx - 1 (its row counts as 0).
+ * Rules: K % 16 == 0, N % 16 == 0, 1 <= E <= 512; S == 0 returns QG_OK.
+ * workspace: as for qg_gemm_fp8, of qg_workspace_size(QG_OP_GEMM_FP8_EXPERTS, S, K, N). */
+qg_status qg_gemm_fp8_experts(const uint8_t* Xq, const float* xs, int Mx, int K,
+                              const int32_t* slot_token, const int32_t* offsets, int S, int E,
+                              const uint8_t* Wq, const float* ws, int N, void* Y, qg_dtype ydt,
+                              void* workspace, size_t ws_bytes, qg_stream_t stream);
+
+/* Back to the tokens:  Y[m] = rn( sum_j weights[m][j] * D[token_slot[m][j]] )  (fp32, j in
+ * order); a choice of slot -1 adds nothing (its weight is not read into the sum), a token
+ * with none gets 0.
+ * D fp16 or bf16 [S][N], Y the same type [M][N]; token_slot int32 [M][topk]; weights fp32
+ * [M][topk].  Rules: N % 8 == 0, topk >= 1.
+ * Device error: QG_ERR_RANGE (a slot outside -1 .. S-1, which adds nothing). */
+qg_status qg_combine_experts(const void* D, qg_dtype dt, int S, int N, const int32_t* token_slot,
+                             const float* weights, int M, int topk, void* Y, qg_stream_t stream);
+
 /* Bytes of workspace the given operation and shape can use (0 = none).  The
  * value depends only on (op, M, K, N) and on the current device.  For
- * QG_OP_AWQ_SEARCH, M is the calibration token count Mc. */
+ * QG_OP_AWQ_SEARCH, M is the calibration token count Mc; for QG_OP_GEMM_FP8_EXPERTS,
+ * M is S; for QG_OP_EXPERT_SLOTS, K is topk and N is E. */
 size_t qg_workspace_size(qg_op op, int M, int K, int N);
 
 /* --------------------------------------------------------------------------
