@@ -33,7 +33,76 @@ qg_status quantize_weight_fp8(const void* W, int E, int K, int N, uint8_t* Wq, f
 // ---------------------------------------------------------------------------
 bool fp8_bad_shape(int K, int N) { return K < 16 || K % 16 || N < 16 || N % 16; }
 
-size_t fp8_workspace(int M, int K, int N, bool experts) { return 0; }
+// Rows per tile of the stream kernel for so many rows (an expert's on average), 0: the tile
+// kernel.
+int fp8_stream_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 256 ? 128 : 0; }
+
+struct Fp8Workspace {
+    size_t counters, bytes;
+};
+
+Fp8Workspace fp8_stream_workspace(int nt)
+{
+    const size_t grid = num_sms(), c = (grid * 8 + 255) / 256 * 256;
+    return {c, c + grid * 2 * nt * 128 * sizeof(float)};
+}
+
+// A size that serves every number of experts, for the experts' product.
+size_t fp8_workspace(int M, bool experts)
+{
+    const int nt = experts && M > 64 ? 128 : fp8_stream_rows(M);
+    return nt ? fp8_stream_workspace(nt).bytes : 0;
+}
+
+// The weights as {N, K, E} (boxes of 128 columns x 128 k), the activations as {K, Mx}
+// (boxes of 128 k x `box` rows; 1: gathered).
+qg_status fp8_maps(CUtensorMap* tw, CUtensorMap* tx, const uint8_t* Xq, const uint8_t* Wq, const qg::Fp8Params& p, int box)
+{
+    const uint64_t N = p.N, K = p.K;
+    qg_status st = make_tmap_3d(tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq, N, K, p.E, N, N * K, 128, 128, 1,
+                                CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != QG_OK) return st;
+    return make_tmap_2d(tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Xq, K, p.Mx, 128, p.rows ? 1 : box,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int NT>
+qg_status launch_fp8_stream(qg::Fp8Params p, const uint8_t* Xq, const uint8_t* Wq, void* ws, qg_stream_t stream)
+{
+    using C = qg::Fp8StreamCfg<NT>;
+    auto kern = qg::fp8_stream_kernel<NT>;
+    static KernelInfo info;
+    int occ = 1;
+    qg_status st = prepare_kernel(info, kern, C::THREADS, C::TOTAL, &occ);
+    if (st != QG_OK) return st;
+    CUtensorMap tw, tx;
+    if ((st = fp8_maps(&tw, &tx, Xq, Wq, p, NT)) != QG_OK) return st;
+    p.counters = static_cast<unsigned long long*>(ws);
+    p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + fp8_stream_workspace(NT).counters);
+    do p.token = next_decode_token() << 8;
+    while (p.token == 0);
+    int grid = num_sms();
+    if (!p.offsets) grid = (int)std::min<int64_t>(grid, (int64_t)((p.S + NT - 1) / NT) * ((p.N + 127) / 128) * p.G);
+    return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::TOTAL, stream, p, tw, tx);
+}
+
+qg_status launch_fp8_tile(const qg::Fp8Params& p, const uint8_t* Xq, const uint8_t* Wq, qg_stream_t stream)
+{
+    using C = qg::Fp8TileCfg;
+    auto kern = qg::fp8_tile_kernel;
+    static KernelInfo info;
+    int occ = 1;
+    qg_status st = prepare_kernel(info, kern, C::THREADS, C::TOTAL, &occ);
+    if (st != QG_OK) return st;
+    CUtensorMap tw, tx;
+    if ((st = fp8_maps(&tw, &tx, Xq, Wq, p, C::BM)) != QG_OK) return st;
+    // at most so many tiles: every expert may end inside one
+    const int64_t rows = (int64_t)(p.S + C::BM - 1) / C::BM + (p.offsets ? std::min(p.S, p.E) : 0);
+    const int grid = (int)std::min<int64_t>(num_sms(), rows * ((p.N + C::BN - 1) / C::BN));
+    kern<<<grid, C::THREADS, C::TOTAL, reinterpret_cast<cudaStream_t>(stream)>>>(p, tw, tx);
+    QG_CUDA(cudaGetLastError());
+    return QG_OK;
+}
 
 qg_status fp8_gemm(const uint8_t* Xq, const float* xs, int Mx, int K, const int32_t* rows, const int32_t* offsets, int S,
                    int E, const uint8_t* Wq, const float* ws, int N, void* Y, qg_dtype ydt, void* workspace,
@@ -43,15 +112,30 @@ qg_status fp8_gemm(const uint8_t* Xq, const float* xs, int Mx, int K, const int3
     if (misaligned(Xq) || misaligned(xs) || misaligned(rows) || misaligned(offsets) || misaligned(Wq) ||
         misaligned(ws) || misaligned(Y) || misaligned(workspace))
         return QG_ERR_ALIGN;
-    const size_t need = fp8_workspace(S, K, N, offsets != nullptr);
+    const size_t need = fp8_workspace(S, offsets != nullptr);
     if (need && !workspace) return QG_ERR_NULL;
     if (need > ws_bytes) return QG_ERR_WORKSPACE;
-    const qg::Fp8Params p{Xq, xs, Wq, ws, rows, offsets, static_cast<uint16_t*>(Y), Mx, S, E, K, N,
-                          (K + 127) / 128, (N + 127) / 128, ydt == QG_BF16};
-    const int tiles = offsets ? S / 64 + std::min(S, E) : (S + 63) / 64;
-    qg::fp8_gemm_simple_kernel<<<dim3((N + 63) / 64, tiles), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    QG_CUDA(cudaGetLastError());
-    return QG_OK;
+    qg::Fp8Params p{};
+    p.xs = xs;
+    p.ws = ws;
+    p.rows = rows;
+    p.offsets = offsets;
+    p.Y = static_cast<uint16_t*>(Y);
+    p.Mx = Mx;
+    p.S = S;
+    p.E = E;
+    p.K = K;
+    p.N = N;
+    p.G = (K + 127) / 128;
+    p.NB = (N + 127) / 128;
+    p.bf16 = ydt == QG_BF16;
+    switch (fp8_stream_rows(offsets ? ((int64_t)S + E - 1) / E : S)) {
+        case 16: return launch_fp8_stream<16>(p, Xq, Wq, workspace, stream);
+        case 32: return launch_fp8_stream<32>(p, Xq, Wq, workspace, stream);
+        case 64: return launch_fp8_stream<64>(p, Xq, Wq, workspace, stream);
+        case 128: return launch_fp8_stream<128>(p, Xq, Wq, workspace, stream);
+        default: return launch_fp8_tile(p, Xq, Wq, stream);
+    }
 }
 
 // ---------------------------------------------------------------------------

@@ -333,6 +333,7 @@ COUNTS = {
     "tiles": [128, 0, 129, 127, 1, 256, 300],
     "even": [40] * 12,
     "many": [3] * 100,
+    "large": [700, 0, 513, 300],
 }
 
 
