@@ -36,7 +36,7 @@ struct Fp8Params {
     bool bf16;
     // stream kernel: the workspace
     unsigned long long* counters;  // [grid]
-    float* partials;               // [grid][2][NT][128]
+    float* partials;               // [grid][2][NT][256]
     unsigned long long token;      // this launch's token (its low byte is 0, the rest is not)
 };
 
@@ -74,10 +74,37 @@ QG_DEV_INLINE void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.
 template <int R>
 QG_DEV_INLINE void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
+// A bounded wait like mbar_wait's that looks at the clock and the limit only after many polls:
+// here a wait is mostly a few hundred cycles long and lies on the chain between the tensor core
+// and the warps that fold.
+QG_DEV_INLINE bool short_wait(uint64_t* bar, uint32_t parity)
+{
+    for (uint32_t it = 0; it < 256; ++it)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait(bar, parity);
+}
+
+// One lane of the (converged) warp.  The role loops below run warp-uniform and only the TMA,
+// MMA and commit instructions are the elected lane's: the compiler then keeps descriptors in
+// uniform registers.  In code that a whole branch gives to one lane an MMA took 110 issue
+// cycles (512 cycles of MMA a step became 900 beside the folding warps).
+QG_DEV_INLINE bool elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+QG_DEV_INLINE int uniform_warp() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
+
 // every lane waits; the result is the warp's
 QG_DEV_INLINE bool all_wait(uint64_t* bar, uint32_t parity)
 {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+    return __all_sync(0xffffffffu, short_wait(bar, parity));
 }
 
 // ---------------------------------------------------------------------------
@@ -177,37 +204,153 @@ QG_DEV_INLINE void fp8_gather_rows(const Fp8Params& p, int s0, int rows, int lan
 QG_DEV_INLINE uint16_t fp8_out(const Fp8Params& p, float v) { return p.bf16 ? f32_to_bf16_bits(v) : f32_to_f16_bits(v); }
 QG_DEV_INLINE uint32_t fp8_out2(const Fp8Params& p, float a, float b) { return p.bf16 ? pack_bf16x2_rn(a, b) : pack_f16x2_rn(a, b); }
 
+// The scales of a run of units (tiles of T rows x 256 columns), four groups at a time: a lane holds R rows, the four groups in
+// use and, loading, the four after them, so that a load has four units' time to arrive.  (One
+// load per unit, four units ahead, was slower: a wait for one of them waited for all.)
+template <int T, int R>
+struct Fp8Scales {
+    const Fp8Params& p;
+    Fp8Walk<T> walk;      // of the tile being loaded
+    int64_t left;         // units not yet loaded
+    int lane, kb;         // first group not yet loaded
+    int row[R];
+    const float* wsp;     // the tile's first weight scale
+    bool wide;            // its second 128 columns exist
+    float x[R][4], w[2][4], nx[R][4], nw[2][4];
+    int n, nn;            // groups held and loading
+
+    QG_DEV_INLINE Fp8Scales(const Fp8Params& p_, const Fp8Walk<T>& w_, int64_t units, int kb0, int lane_)
+        : p(p_), walk(w_), left(units), lane(lane_), kb(kb0), n(0), nn(0)
+    {
+        tile();
+        load();
+    }
+    QG_DEV_INLINE void tile()
+    {
+        const int s0 = walk.first(), rows = walk.rows();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = lane + 32 * r;
+            row[r] = t < rows ? fp8_row(p, s0 + t) : -2;
+            if (row[r] == -1) set_status(6u);
+        }
+        wsp = p.ws + (int64_t)walk.e * p.G * p.NB + 2 * walk.slab;
+        wide = 2 * walk.slab + 1 < p.NB;
+    }
+    QG_DEV_INLINE void load()
+    {
+        nn = (int)min((int64_t)min(4 - (kb & 3), p.G - kb), left);
+        if (nn == 0) return;
+        const bool vec = p.G % 4 == 0;   // then every row starts on 16 bytes
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float* src = p.xs + (int64_t)max(row[r], 0) * p.G + kb;
+            if (vec && nn == 4) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(src));
+                nx[r][0] = v.x; nx[r][1] = v.y; nx[r][2] = v.z; nx[r][3] = v.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) nx[r][j] = j < nn ? __ldg(src + j) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float* src = wsp + (int64_t)(kb + j) * p.NB;
+            nw[0][j] = j < nn ? __ldg(src) : 0.0f;
+            nw[1][j] = j < nn && wide ? __ldg(src + 1) : 0.0f;
+        }
+    }
+    // The loaded groups become those in use, the next ones are requested; false: none left.
+    QG_DEV_INLINE bool advance()
+    {
+        n = nn;
+        if (n == 0) return false;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[r][j] = row[r] >= 0 ? nx[r][j] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[0][j] = nw[0][j];
+            w[1][j] = nw[1][j];
+        }
+        left -= n;
+        kb += n;
+        if (kb == p.G) {
+            kb = 0;
+            if (left > 0) {
+                walk.next();
+                tile();
+            }
+        }
+        load();
+        return true;
+    }
+};
+
+// acc[0 .. CW) += (CW sums of tensor memory at `addr`) * scale, where the scale of sum t is
+// sv[t] (shared memory, 16-byte aligned; PER = true) or the one number sc.  Sixteen columns at a
+// time, the next ones' load in flight while the ones before are folded; `release` runs once all
+// are read (PER: and their scales too).
+template <int CW, bool PER, typename F>
+QG_DEV_INLINE void fp8_fold(float (&acc)[CW], uint32_t addr, const float* sv, float sc, F release)
+{
+    uint32_t v[2][16];
+    tmem_ld_32x32b_x16(addr, v[0]);
+#pragma unroll
+    for (int c = 0; c < CW; c += 16) {
+        uint32_t(&u)[16] = v[(c / 16) & 1];
+        tmem_ld_wait();
+#pragma unroll
+        for (int t = 0; t < 16; ++t) asm volatile("" : "+r"(u[t]));   // read only after the wait
+        if (c + 16 < CW) tmem_ld_32x32b_x16(addr + c + 16, v[(c / 16 + 1) & 1]);
+        else if (!PER) release();
+#pragma unroll
+        for (int t = 0; t < 16; t += 4) {
+            float4 s4 = make_float4(sc, sc, sc, sc);
+            if constexpr (PER) s4 = *reinterpret_cast<const float4*>(sv + c + t);
+            acc[c + t] = fmaf(__uint_as_float(u[t]), s4.x, acc[c + t]);
+            acc[c + t + 1] = fmaf(__uint_as_float(u[t + 1]), s4.y, acc[c + t + 1]);
+            acc[c + t + 2] = fmaf(__uint_as_float(u[t + 2]), s4.z, acc[c + t + 2]);
+            acc[c + t + 3] = fmaf(__uint_as_float(u[t + 3]), s4.w, acc[c + t + 3]);
+        }
+    }
+    if (PER) release();
+}
+
 // ---------------------------------------------------------------------------
 // Few rows: stream-K
 //
-// Units are (tile, group of K); CTA c takes units [c U / grid, (c + 1) U / grid).  A tile
-// whose units lie in several CTAs is joined by whichever of them arrives last: each leaves
-// its fp32 sums in the workspace and counts itself in; the last one adds all of them in CTA
-// order (the result does not depend on who is last) and writes Y.  No CTA waits for another.
-// The counter word holds the launch's token above an 8-bit count, so whatever an unused
-// workspace holds reads as 0, and the last arrival clears it, so a replayed graph finds it
-// so again.
+// Tiles of NT rows x 256 columns (256 so that a weight row is read 256 bytes at a time: with
+// 128-byte boxes DRAM read 1.37 times the weights).  Units are (tile, group of K); CTA c takes
+// units [c U / grid, (c + 1) U / grid).  A tile whose units lie in several CTAs is joined by
+// whichever of them arrives last: each leaves its fp32 sums in the workspace and counts itself
+// in; the last one adds all of them in CTA order (the result does not depend on who is last)
+// and writes Y.  No CTA waits for another.  The counter word holds the launch's token above an
+// 8-bit count, so whatever an unused workspace holds reads as 0, and the last arrival clears
+// it, so a replayed graph finds it so again.
 //
-// Roles: warp 0 TMA; warp 1 issues the MMAs (each unit into one of four buffers); warp 2
-// multiplies the scales (four units ahead in registers) into the buffer's slot; warps 4..
-// fold the units (thread = column).
+// Roles: warp 0 TMA; warp 1 issues the MMAs (the 128-column halves are M, the rows N; each
+// unit into one of DB buffers); warp 2 writes the units' scales; warps 4..11 fold the units
+// (thread = column).
 // ---------------------------------------------------------------------------
 template <int NT>
 struct Fp8StreamCfg {
-    static constexpr int W_BYTES = 128 * 128, X_BYTES = NT * 128;
+    static constexpr int W_BYTES = 2 * 128 * 128, X_BYTES = NT * 128;
     static constexpr int STAGE = W_BYTES + X_BYTES;
-    static constexpr int ST = NT == 16 ? 10 : NT == 32 ? 9 : NT == 64 ? 8 : 6;
-    static constexpr int DB = 4;                    // buffers of sums and scales
-    static constexpr int EPI = NT == 128 ? 8 : 4;   // epilogue warps
-    static constexpr int CW = NT * 4 / EPI;         // rows of the tile per epilogue thread
+    static constexpr int ST = NT <= 32 ? 6 : 4;     // even: a stage always serves the same issuer
+    static constexpr int DB = NT == 128 ? 2 : 4;    // buffers of sums [2][NT]
+    static constexpr int SC = 8;                    // slots of scales [2][NT]
+    static constexpr int EPI = 8;
     static constexpr int THREADS = 32 * (4 + EPI);
-    static constexpr int TMEM_COLS = DB * NT;
+    static constexpr int TMEM_COLS = DB * 2 * NT;
     static constexpr int SC_OFF = ST * STAGE;
-    static constexpr int SCHED_OFF = SC_OFF + DB * NT * 4;
+    static constexpr int SCHED_OFF = SC_OFF + SC * 2 * NT * 4;
     static constexpr int BAR_OFF = SCHED_OFF + (int)((sizeof(Fp8Sched) + 15) / 16 * 16);
-    static constexpr int NBAR = 2 * ST + 2 * DB + 1;
+    static constexpr int NBAR = 2 * ST + 2 * DB + 2 * SC + 2;
     static constexpr int TOTAL = BAR_OFF + NBAR * 8 + 16 + 1024;
-    static_assert(STAGE % 1024 == 0 && TOTAL <= 227 * 1024, "stream kernel shared memory");
+    static constexpr int PARTIAL = NT * 256;        // floats of a piece's sums
+    static_assert(STAGE % 1024 == 0 && TOTAL <= 227 * 1024 - 64 && ST % 2 == 0, "stream kernel shared memory");
 };
 
 QG_DEV_INLINE int64_t fp8_first_unit(int c, int64_t units, int grid) { return c * units / grid; }
@@ -239,21 +382,23 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, 1)
                       const __grid_constant__ CUtensorMap tm_x)
 {
     using C = Fp8StreamCfg<NT>;
-    constexpr int ST = C::ST, DB = C::DB;
+    constexpr int ST = C::ST, DB = C::DB, SC = C::SC;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);   // [DB][NT]
+    float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);   // [SC][2][NT]
     Fp8Sched& sched = *reinterpret_cast<Fp8Sched*>(smem + C::SCHED_OFF);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
     uint64_t* empty = full + ST;
-    uint64_t* dfull = empty + ST;     // the buffer's sums (the MMAs' commit) and scales (warp 2)
+    uint64_t* dfull = empty + ST;
     uint64_t* dempty = dfull + DB;
-    uint64_t* done = dempty + DB;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+    uint64_t* sfull = dempty + DB;
+    uint64_t* sempty = sfull + SC;
+    uint64_t* done = sempty + SC;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 2);
     __shared__ int s_last;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = p.G, slabs = (p.N + 127) / 128;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    const int G = p.G, slabs = (p.N + 255) / 256;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
@@ -262,10 +407,15 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, 1)
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < DB; ++i) {
-            mbar_init(&dfull[i], 2);
+            mbar_init(&dfull[i], 1);
             mbar_init(&dempty[i], C::EPI);
         }
-        mbar_init(done, 1);
+        for (int i = 0; i < SC; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&sempty[i], C::EPI);
+        }
+        mbar_init(&done[0], 1);
+        mbar_init(&done[1], 1);
         fence_mbar_init();
         tma_prefetch_desc(&tm_w);
         tma_prefetch_desc(&tm_x);
@@ -290,182 +440,151 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, 1)
 
     Fp8Walk<NT> walk(sched, p.E, slabs);
     walk.at(tile0);
-    if (warp == 0) {
-        // ---------------- producer ----------------
-        int kb = kb0, i = 0, y[4];
-        const int early = p.offsets ? 0 : min(ST, n_it);
-        if (early) {
-            // weights do not depend on the kernel before: the ring's first are requested
-            // before waiting for it
-            Fp8Walk<NT> w = walk;
-            for (int j = 0, k = kb0; j < early; ++j) {
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[j], C::STAGE);
-                    tma_load_3d(&tm_w, &full[j], smem + j * C::STAGE, w.slab * 128, k * 128, w.e);
+    if (warp < 4) {
+        if constexpr (NT == 128) setmaxnreg_dec<72>();
+        if (warp == 0) {
+            // ---------------- producer ----------------
+            int kb = kb0, i = 0, y[4];
+            const bool one = elect_one();
+            const int early = p.offsets ? 0 : min(ST, n_it);
+            auto weights = [&](int s, const Fp8Walk<NT>& w, int k) {
+                uint8_t* st = smem + s * C::STAGE;
+                mbar_arrive_expect_tx(&full[s], C::STAGE);
+                tma_load_3d(&tm_w, &full[s], st, w.slab * 256, k * 128, w.e);
+                tma_load_3d(&tm_w, &full[s], st + 16384, w.slab * 256 + 128, k * 128, w.e);
+            };
+            if (early) {
+                // weights do not depend on the kernel before: the ring's first are requested
+                // before waiting for it
+                Fp8Walk<NT> w = walk;
+                for (int j = 0, k = kb0; j < early; ++j) {
+                    if (one) weights(j, w, k);
+                    if (++k == G) { k = 0; w.next(); }
                 }
-                if (++k == G) { k = 0; w.next(); }
+                asm volatile("griddepcontrol.wait;" ::: "memory");
             }
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-        }
-        if (p.rows) fp8_gather_rows(p, walk.first(), walk.rows(), lane, y);
-        bool ok = true;
-        for (; i < n_it; ++i) {
-            const int s = i % ST;
-            uint8_t* st = smem + s * C::STAGE;
-            if (i >= early) {
-                ok = all_wait(&empty[s], ((i / ST) & 1) ^ 1);
-                if (!ok) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[s], C::STAGE);
-                    tma_load_3d(&tm_w, &full[s], st, walk.slab * 128, kb * 128, walk.e);
-                }
-                __syncwarp();
-            }
-            if (!p.rows) {
-                if (lane == 0) tma_load_2d(&tm_x, &full[s], st + C::W_BYTES, kb * 128, walk.first());
-            } else if (lane < NT / 4) {
-                tma_gather4(&tm_x, &full[s], st + C::W_BYTES + lane * 512, kb * 128, y);
-            }
-            if (++kb == G) {
-                kb = 0;
-                walk.next();
-                if (p.rows && i + 1 < n_it) fp8_gather_rows(p, walk.first(), walk.rows(), lane, y);
-            }
-        }
-        if (!ok)   // copies in flight land before the block leaves
-            for (int j = max(i - ST, 0); j < i; ++j) all_wait(&full[j % ST], (j / ST) & 1);
-    } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_e4m3(NT, true, false);
-            int i = 0;
+            if (p.rows) fp8_gather_rows(p, walk.first(), walk.rows(), lane, y);
+            bool ok = true;
             for (; i < n_it; ++i) {
-                const int s = i % ST, b = i % DB;
-                if (!mbar_wait(&dempty[b], ((i / DB) & 1) ^ 1) || !mbar_wait(&full[s], (i / ST) & 1)) break;
-                tc_fence_after();
-                const uint32_t w = smem_u32(smem + s * C::STAGE), x = w + C::W_BYTES;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_e4m3_ss(tmem + b * NT, smem_desc(w + 4096 * kk, 16384, 1024, 2),
-                                smem_desc(x + 32 * kk, 16, 1024, 2), idesc, kk > 0 ? 1u : 0u);
-                mma_commit(&empty[s]);
-                mma_commit(&dfull[b]);
-            }
-            if (i > 0) {   // every MMA has completed before tensor memory is released
-                mma_commit(done);
-                mbar_wait(done, 0);
-            }
-        }
-    } else if (warp == 2) {
-        // ---------------- scales ----------------
-        if (!p.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
-        constexpr int R = (NT + 31) / 32, AHEAD = 4;
-        static_assert(AHEAD == DB, "one register set per buffer");
-        int row[R], kb = kb0;
-        float x[AHEAD][R], w[AHEAD];
-        const float* wsp = nullptr;
-        auto tile_rows = [&]() {
-            const int s0 = walk.first(), rows = walk.rows();
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int t = lane + 32 * r;
-                row[r] = t < rows ? fp8_row(p, s0 + t) : -2;
-                if (row[r] == -1) set_status(6u);
-            }
-            wsp = p.ws + (int64_t)walk.e * G * p.NB + walk.slab;
-        };
-        auto load = [&](int slot) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) x[slot][r] = row[r] >= 0 ? __ldg(p.xs + (int64_t)row[r] * G + kb) : 0.0f;
-            w[slot] = __ldg(wsp + (int64_t)kb * p.NB);
-        };
-        auto step = [&](bool more) {
-            if (++kb == G) {
-                kb = 0;
-                if (more) {
+                const int s = i % ST;
+                if (i >= early) {
+                    ok = all_wait(&empty[s], ((i / ST) & 1) ^ 1);
+                    if (!ok) break;
+                    if (one) weights(s, walk, kb);
+                    __syncwarp();
+                }
+                uint8_t* xt = smem + s * C::STAGE + C::W_BYTES;
+                if (!p.rows) {
+                    if (one) tma_load_2d(&tm_x, &full[s], xt, kb * 128, walk.first());
+                } else if (lane < NT / 4) {
+                    tma_gather4(&tm_x, &full[s], xt + lane * 512, kb * 128, y);
+                }
+                if (++kb == G) {
+                    kb = 0;
                     walk.next();
-                    tile_rows();
+                    if (p.rows && i + 1 < n_it) fp8_gather_rows(p, walk.first(), walk.rows(), lane, y);
                 }
             }
-        };
-        tile_rows();
-        int ahead = 0;
+            if (!ok)   // copies in flight land before the block leaves
+                for (int j = max(i - ST, 0); j < i; ++j) all_wait(&full[j % ST], (j / ST) & 1);
+        } else if (warp & 1) {
+            // ------- MMA issuers: warp 1 the even units, warp 3 the odd ones, so that one's waits
+            // lie beside the other's MMAs -------
+            constexpr uint32_t idesc = idesc_e4m3(NT, true, false);
+            const uint64_t w0 = smem_desc(smem_u32(smem), 16384, 1024, 2), x0 = smem_desc(smem_u32(smem + C::W_BYTES), 16, 1024, 2);
+            const bool one = elect_one();
+            const int e = warp >> 1;
+            int i = e, s = e, b = e;
+            uint32_t sp = 0, bp = 1;   // parities
+            for (; i < n_it; i += 2) {
+                if (!all_wait(&full[s], sp) || !all_wait(&dempty[b], bp)) break;
+                tc_fence_after();
+                if (one) {
+                    const uint64_t w = w0 + s * (C::STAGE >> 4), x = x0 + s * (C::STAGE >> 4);
+                    const uint32_t d = tmem + 2 * b * NT;
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a)
-            if (ahead < n_it) {
-                load(a);
-                ++ahead;
-                step(ahead < n_it);
-            }
-        bool ok = true;
-        for (int i0 = 0; i0 < n_it && ok; i0 += AHEAD) {
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int b = 0; b < AHEAD; ++b) {
-                if (i0 + b >= n_it || !ok) break;
-                ok = all_wait(&dempty[b], ((i0 / DB) & 1) ^ 1);
-                if (!ok) break;
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (lane + 32 * r < NT) scales[b * NT + lane + 32 * r] = __fmul_rn(x[b][r], w[b]);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_e4m3_ss(d + h * NT, w + h * (16384 >> 4) + kk * (4096 >> 4), x + kk * (32 >> 4), idesc, kk > 0 ? 1u : 0u);
+                    mma_commit(&dfull[b]);
+                    mma_commit(&empty[s]);
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&dfull[b]);
-                if (ahead < n_it) {
-                    load(b);
-                    ++ahead;
-                    step(ahead < n_it);
+                if ((s += 2) >= ST) { s = e; sp ^= 1; }
+                if ((b += 2) >= DB) { b = e; bp ^= 1; }
+            }
+            if (i > 1) {   // every MMA has completed before tensor memory is released
+                if (one) mma_commit(&done[e]);
+                __syncwarp();
+                all_wait(&done[e], 0);
+            }
+        } else if (warp == 2) {
+            // ---------------- scales ----------------
+            if (!p.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
+            constexpr int R = (NT + 31) / 32;
+            Fp8Scales<NT, R> sc(p, walk, n_it, kb0, lane);
+            bool ok = true;
+            int i = 0;
+            while (ok && sc.advance()) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j < sc.n && ok) {
+                        const int b = i % SC;
+                        ok = all_wait(&sempty[b], ((i / SC) & 1) ^ 1);
+                        if (ok) {
+                            float* o = scales + b * 2 * NT;
+#pragma unroll
+                            for (int r = 0; r < R; ++r)
+                                if (lane + 32 * r < NT) {
+                                    o[lane + 32 * r] = __fmul_rn(sc.x[r][j], sc.w[0][j]);
+                                    o[NT + lane + 32 * r] = __fmul_rn(sc.x[r][j], sc.w[1][j]);
+                                }
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sfull[b]);
+                            ++i;
+                        }
+                    }
                 }
             }
         }
-    } else if (warp >= 4) {
-        // ---------------- epilogue: thread = column ----------------
+    } else {
+        if constexpr (NT == 128) setmaxnreg_inc<216>();
+        // ---------------- fold: thread = column ----------------
         asm volatile("griddepcontrol.wait;" ::: "memory");   // Y and the workspace follow the kernel before
-        constexpr int CW = C::CW;
-        const int q = warp & 3, t0 = (warp - 4) / 4 * CW, col = 32 * q + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + t0;
-        float acc[CW];
+        const int q = warp & 3, half = (warp - 4) >> 2, col = half * 128 + 32 * q + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + half * NT;
+        float acc[NT];
         bool ok = true;
         int i = 0, kb = kb0;
         while (i < n_it) {
             const int ie = min(n_it, i + G - kb);   // this piece: units [i, ie)
             const bool head = kb == 0, whole = head && ie - i == G;
+            const int64_t first = u0 + i - kb;      // the tile's first unit
 #pragma unroll
-            for (int t = 0; t < CW; ++t) acc[t] = 0.0f;
-            const int piece0 = i;
+            for (int t = 0; t < NT; ++t) acc[t] = 0.0f;
             for (; i < ie; ++i) {
-                const int b = i % DB;
-                ok = ok && all_wait(&dfull[b], (i / DB) & 1);
+                const int b = i % DB, sl = i % SC;
+                if (ok) ok = all_wait(&sfull[sl], (i / SC) & 1) && all_wait(&dfull[b], (i / DB) & 1);
                 if (!ok) continue;
                 tc_fence_after();
-                const float* sv = scales + b * NT + t0;
-                constexpr int CH = CW < 32 ? 16 : 32;
-#pragma unroll
-                for (int c = 0; c < CW; c += CH) {
-                    uint32_t r[CH];
-                    if constexpr (CH == 16) tmem_ld_32x32b_x16(lanes + b * NT + c, r);
-                    else tmem_ld_32x32b_x32(lanes + b * NT + c, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int t = 0; t < CH; t += 4) {
-                        const float4 s4 = *reinterpret_cast<const float4*>(sv + c + t);
-                        acc[c + t] = fmaf(__uint_as_float(r[t]), s4.x, acc[c + t]);
-                        acc[c + t + 1] = fmaf(__uint_as_float(r[t + 1]), s4.y, acc[c + t + 1]);
-                        acc[c + t + 2] = fmaf(__uint_as_float(r[t + 2]), s4.z, acc[c + t + 2]);
-                        acc[c + t + 3] = fmaf(__uint_as_float(r[t + 3]), s4.w, acc[c + t + 3]);
+                fp8_fold<NT, true>(acc, lanes + b * 2 * NT, scales + (2 * sl + half) * NT, 0.0f, [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&dempty[b]);
+                        mbar_arrive(&sempty[sl]);
                     }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&dempty[b]);
+                });
             }
-            const int rows = walk.rows(), s0 = walk.first(), n = walk.slab * 128 + col;
+            const int rows = walk.rows(), s0 = walk.first(), n = walk.slab * 256 + col;
             bool write = whole;
             if (!whole) {
-                float* mine = p.partials + ((int64_t)blockIdx.x * 2 + (head ? 1 : 0)) * NT * 128 + col;
+                float* mine = p.partials + ((int64_t)blockIdx.x * 2 + (head ? 1 : 0)) * C::PARTIAL + col;
 #pragma unroll
-                for (int t = 0; t < CW; ++t)
-                    if (t0 + t < rows) __stcg(mine + (t0 + t) * 128, acc[t]);
-                // pieces of this tile: CTAs cf .. cl
-                const int64_t first = u0 + piece0 - (head ? 0 : kb);
+                for (int t = 0; t < NT; ++t)
+                    if ((t & ~15) < rows) __stcg(mine + t * 256, acc[t]);
+                // the pieces of this tile are CTAs cf .. cl
                 const int cf = head ? (int)blockIdx.x : fp8_cta_of_unit(first, units, grid);
                 const int cl = fp8_cta_of_unit(first + G - 1, units, grid);
                 __threadfence();
@@ -478,23 +597,42 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, 1)
                 write = s_last;
                 if (write) {
 #pragma unroll
-                    for (int t = 0; t < CW; ++t) acc[t] = 0.0f;
+                    for (int t = 0; t < NT; ++t) acc[t] = 0.0f;
                     for (int c = cf; c <= cl; ++c) {
-                        const float* o = p.partials + ((int64_t)c * 2 + (c == cf ? 1 : 0)) * NT * 128 + col;
+                        const float* o = p.partials + ((int64_t)c * 2 + (c == cf ? 1 : 0)) * C::PARTIAL + col;
 #pragma unroll
-                        for (int t = 0; t < CW; ++t)
-                            if (t0 + t < rows) acc[t] += __ldcg(o + (t0 + t) * 128);
+                        for (int t0 = 0; t0 < NT; t0 += 16) {   // 16 loads in flight
+                            if (t0 < rows) {
+                                float v[16];
+#pragma unroll
+                                for (int t = 0; t < 16; ++t) v[t] = __ldcg(o + (t0 + t) * 256);
+#pragma unroll
+                                for (int t = 0; t < 16; ++t) acc[t0 + t] += v[t];
+                            }
+                        }
                     }
                 }
                 named_bar_sync(1, 32 * C::EPI);   // s_last has been read
             }
-            if (write && ok && n < p.N) {
+            if (write && ok) {
+                uint32_t zero[(NT + 31) / 32];   // rows whose map entry is wrong
 #pragma unroll
-                for (int t = 0; t < CW; ++t)
-                    if (t0 + t < rows) {
-                        const int s = s0 + t0 + t;
-                        p.Y[(int64_t)s * p.N + n] = fp8_row(p, s) < 0 ? 0 : fp8_out(p, acc[t]);
-                    }
+                for (int r = 0; r < (NT + 31) / 32; ++r) {
+                    const int t = lane + 32 * r;
+                    zero[r] = p.rows ? __ballot_sync(0xffffffffu, t < rows && fp8_row(p, s0 + t) < 0) : 0u;
+                }
+                // lane pairs exchange, so that a lane stores two adjacent columns of a row
+                const int odd = lane & 1;
+                uint16_t* y = p.Y + (int64_t)(s0 + odd) * p.N + n - odd;
+#pragma unroll
+                for (int t = 0; t < NT; t += 2) {
+                    uint32_t a = fp8_out(p, acc[t]), b = fp8_out(p, acc[t + 1]);
+                    if (zero[t / 32] >> (t & 31) & 1u) a = 0;
+                    if (zero[t / 32] >> ((t + 1) & 31) & 1u) b = 0;
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                    if (t + odd < rows && n < p.N)
+                        *reinterpret_cast<uint32_t*>(y + (int64_t)t * p.N) = odd ? got | b << 16 : a | got << 16;
+                }
             }
             kb = 0;
             walk.next();
@@ -510,60 +648,55 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: 128 rows x 256 columns, one group of K a step, persistent.
+// Many rows: 128 rows x BN columns, one group of K a step, persistent.
 //
-// Two 256-column buffers alternate from step to step.  Roles: warp 0 TMA, warp 1 MMA, warps
-// 2 and 3 the scales (two rows a lane, four groups ahead), warps 4..11 fold: warp e holds
-// rows 32 (e % 4) .. + 31 (thread = row) and 128 of the columns, whose weight scale is one
-// number, so a step costs a thread one scale and 128 fma.
+// Roles: warp 0 TMA; warps 1 and 3 issue the MMAs, step by step into DB buffers; warps 4..11
+// fold: thread = row, BN / 2 columns, whose weight scale is one number, so a step costs a thread
+// one scale (which it loads itself) and BN / 2 fma.
 // ---------------------------------------------------------------------------
+template <int BN>
 struct Fp8TileCfg {
-    static constexpr int BM = 128, BN = 256;
-    static constexpr int A_BYTES = 128 * 128, B_BYTES = 256 * 128, STAGE = A_BYTES + B_BYTES, ST = 4;
-    static constexpr int SC = 8;   // slots of scales [2][128]
-    static constexpr int THREADS = 384, TMEM_COLS = 512;
-    static constexpr int SC_OFF = ST * STAGE;
-    static constexpr int SCHED_OFF = SC_OFF + SC * 256 * 4;
+    static constexpr int BM = 128, DB = 512 / BN;
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
+    static constexpr int ST = BN == 256 ? 4 : 6;
+    static constexpr int THREADS = 384;
+    static constexpr int OUT_OFF = ST * STAGE;            // per fold warp: 32 rows x 32 columns of Y
+    static constexpr int SCHED_OFF = OUT_OFF + 8 * 32 * 64;
     static constexpr int BAR_OFF = SCHED_OFF + (int)((sizeof(Fp8Sched) + 15) / 16 * 16);
-    static constexpr int NBAR = 2 * ST + 4 + 2 * SC + 1;
+    static constexpr int NBAR = 2 * ST + 2 * DB + 2;
     static constexpr int TOTAL = BAR_OFF + NBAR * 8 + 16 + 1024;
-    static_assert(TOTAL <= 227 * 1024, "tile kernel shared memory");
+    static_assert(TOTAL <= 227 * 1024 && ST % 2 == 0, "tile kernel shared memory");
 };
 
-__global__ void __launch_bounds__(Fp8TileCfg::THREADS, 1)
+template <int BN>
+__global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
     fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x)
 {
-    using C = Fp8TileCfg;
-    constexpr int ST = C::ST, SC = C::SC;
+    using C = Fp8TileCfg<BN>;
+    constexpr int ST = C::ST, DB = C::DB, HW = BN / 2;   // HW: columns of a fold warp
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);   // [SC][2][128]
     Fp8Sched& sched = *reinterpret_cast<Fp8Sched*>(smem + C::SCHED_OFF);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
     uint64_t* empty = full + ST;
     uint64_t* dfull = empty + ST;
-    uint64_t* dempty = dfull + 2;
-    uint64_t* sfull = dempty + 2;
-    uint64_t* sempty = sfull + SC;
-    uint64_t* done = sempty + SC;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 1);
+    uint64_t* dempty = dfull + DB;
+    uint64_t* done = dempty + DB;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 2);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = p.G, slabs = (p.N + 255) / 256;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    const int G = p.G, slabs = (p.N + BN - 1) / BN;
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < DB; ++i) {
             mbar_init(&dfull[i], 1);
             mbar_init(&dempty[i], 8);
         }
-        for (int i = 0; i < SC; ++i) {
-            mbar_init(&sfull[i], 2);
-            mbar_init(&sempty[i], 8);
-        }
-        mbar_init(done, 1);
+        mbar_init(&done[0], 1);
+        mbar_init(&done[1], 1);
         fence_mbar_init();
         tma_prefetch_desc(&tm_w);
         tma_prefetch_desc(&tm_x);
@@ -572,7 +705,7 @@ __global__ void __launch_bounds__(Fp8TileCfg::THREADS, 1)
     const int tiles = sched.pre[p.E];
     if ((int)blockIdx.x >= tiles) return;
     if (warp == 1) {
-        tmem_alloc(tslot, C::TMEM_COLS);
+        tmem_alloc(tslot, C::DB * BN);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -586,146 +719,147 @@ __global__ void __launch_bounds__(Fp8TileCfg::THREADS, 1)
         if (warp == 0) {
             // ---------------- producer ----------------
             int i = 0, y[4];
+            const bool one = elect_one();
             bool ok = true;
             for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
                 walk.at(tile);
-                const int s0 = walk.first(), n0 = walk.slab * 256;
+                const int s0 = walk.first(), n0 = walk.slab * BN;
                 if (p.rows) fp8_gather_rows(p, s0, walk.rows(), lane, y);
                 for (int kb = 0; kb < G; ++kb, ++i) {
                     const int s = i % ST;
                     ok = all_wait(&empty[s], ((i / ST) & 1) ^ 1);
                     if (!ok) break;
                     uint8_t* st = smem + s * C::STAGE;
-                    if (lane == 0) {
+                    if (one) {
                         mbar_arrive_expect_tx(&full[s], C::STAGE);
                         tma_load_3d(&tm_w, &full[s], st + C::A_BYTES, n0, kb * 128, walk.e);
-                        tma_load_3d(&tm_w, &full[s], st + C::A_BYTES + 16384, n0 + 128, kb * 128, walk.e);
+                        if (BN == 256) tma_load_3d(&tm_w, &full[s], st + C::A_BYTES + 16384, n0 + 128, kb * 128, walk.e);
                         if (!p.rows) tma_load_2d(&tm_x, &full[s], st, kb * 128, s0);
                     }
                     __syncwarp();
                     if (p.rows) tma_gather4(&tm_x, &full[s], st + lane * 512, kb * 128, y);
                 }
             }
-            if (!ok)
+            if (!ok)   // copies in flight land before the block leaves
                 for (int j = max(i - ST, 0); j < i; ++j) all_wait(&full[j % ST], (j / ST) & 1);
-        } else if (warp == 1) {
-            // ---------------- MMA issuer ----------------
-            if (lane == 0) {
-                constexpr uint32_t idesc = idesc_e4m3(256, false, true);
-                bool ok = true;
-                int i = 0;
-                for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x)
-                    for (int kb = 0; kb < G; ++kb, ++i) {
-                        const int s = i % ST, b = i & 1;
-                        if (!mbar_wait(&dempty[b], ((i >> 1) & 1) ^ 1) || !mbar_wait(&full[s], (i / ST) & 1)) { ok = false; break; }
-                        tc_fence_after();
-                        const uint32_t a0 = smem_u32(smem + s * C::STAGE), b0 = a0 + C::A_BYTES;
+        } else if (warp & 1) {
+            // ------- MMA issuers: warp 1 the even units, warp 3 the odd ones, so that one's waits
+            // lie beside the other's MMAs -------
+            constexpr uint32_t idesc = idesc_e4m3(BN, false, true);
+            const uint64_t a0 = smem_desc(smem_u32(smem), 16, 1024, 2);
+            const uint64_t b0 = smem_desc(smem_u32(smem + C::A_BYTES), 16384, 1024, 2);
+            const bool one = elect_one();
+            const int64_t steps = (int64_t)((tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * G;
+            const int e = warp >> 1;
+            int64_t i = e;
+            int s = e, b = e;
+            uint32_t sp = 0, bp = 1;   // parities
+            for (; i < steps; i += 2) {
+                if (!all_wait(&full[s], sp) || !all_wait(&dempty[b], bp)) break;
+                tc_fence_after();
+                if (one) {
+                    const uint64_t ad = a0 + s * (C::STAGE >> 4), bd = b0 + s * (C::STAGE >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_e4m3_ss(tmem + b * 256, smem_desc(a0 + 32 * kk, 16, 1024, 2),
-                                        smem_desc(b0 + 4096 * kk, 16384, 1024, 2), idesc, kk > 0 ? 1u : 0u);
-                        mma_commit(&empty[s]);
-                        mma_commit(&dfull[b]);
-                    }
-                if (i > 0) {
-                    mma_commit(done);
-                    mbar_wait(done, 0);
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_e4m3_ss(tmem + b * BN, ad + kk * (32 >> 4), bd + kk * (4096 >> 4), idesc, kk > 0 ? 1u : 0u);
+                    mma_commit(&dfull[b]);
+                    mma_commit(&empty[s]);
                 }
+                __syncwarp();
+                if ((s += 2) >= ST) { s = e; sp ^= 1; }
+                if ((b += 2) >= DB) { b = e; bp ^= 1; }
             }
-        } else {
-            // ---------------- scales: rows 2 r, 2 r + 1 of r = 0 .. 63 ----------------
-            const int r = threadIdx.x - 64;
-            bool ok = true;
-            int i = 0;
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-                walk.at(tile);
-                const int s0 = walk.first(), rows = walk.rows();
-                int row[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    row[j] = 2 * r + j < rows ? fp8_row(p, s0 + 2 * r + j) : -2;
-                    if (row[j] == -1 && walk.slab == 0) set_status(6u);
-                }
-                const float* w = p.ws + (int64_t)walk.e * G * p.NB + 2 * walk.slab;
-                const bool wide = 2 * walk.slab + 1 < p.NB;
-                float x[4][2], w0[4], w1[4];
-                auto load = [&](int kb, int a) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) x[a][j] = row[j] >= 0 ? __ldg(p.xs + (int64_t)row[j] * G + kb) : 0.0f;
-                    w0[a] = __ldg(w + (int64_t)kb * p.NB);
-                    w1[a] = wide ? __ldg(w + (int64_t)kb * p.NB + 1) : 0.0f;
-                };
-#pragma unroll
-                for (int a = 0; a < 4; ++a)
-                    if (a < G) load(a, a);
-                for (int k0 = 0; k0 < G && ok; k0 += 4) {
-#pragma unroll
-                    for (int a = 0; a < 4; ++a) {
-                        if (k0 + a >= G || !ok) break;
-                        const int s = i % SC;
-                        ok = all_wait(&sempty[s], ((i / SC) & 1) ^ 1);
-                        if (!ok) break;
-                        float2* o = reinterpret_cast<float2*>(scales + s * 256);
-                        o[r] = make_float2(__fmul_rn(x[a][0], w0[a]), __fmul_rn(x[a][1], w0[a]));
-                        o[64 + r] = make_float2(__fmul_rn(x[a][0], w1[a]), __fmul_rn(x[a][1], w1[a]));
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sfull[s]);
-                        ++i;
-                        if (k0 + a + 4 < G) load(k0 + a + 4, a);
-                    }
-                }
+            if (i > 1) {   // every MMA has completed before tensor memory is released
+                if (one) mma_commit(&done[e]);
+                __syncwarp();
+                all_wait(&done[e], 0);
             }
         }
     } else {
         setmaxnreg_inc<216>();
-        // ---------------- fold: thread = row, 128 columns ----------------
-        const int q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + half * 128;
+        // ---------------- fold: thread = row, HW columns ----------------
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + half * HW;
+        uint8_t* out = smem + C::OUT_OFF + (warp - 4) * 2048;
+        const bool vec = G % 4 == 0;   // then every row of xs starts on 16 bytes
+        // the scales of this thread's row and columns, four groups at a time, the next four loading
+        float x[4], w[4];
+        int s0, rows, n0, row;
+        const float *xp, *wp;
+        auto open = [&](int tile) {
+            walk.at(tile);
+            s0 = walk.first() + 32 * q;
+            rows = walk.rows() - 32 * q;
+            n0 = walk.slab * BN + half * HW;
+            row = lane < rows ? fp8_row(p, s0 + lane) : -2;
+            if (row == -1 && walk.slab == 0 && half == 0) set_status(6u);
+            xp = p.xs + (int64_t)max(row, 0) * G;
+            wp = p.ws + (int64_t)walk.e * G * p.NB + min(n0 / 128, p.NB - 1);
+        };
+        auto load = [&](int kb) {
+            if (vec) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(xp + kb));
+                x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = __ldg(xp + min(kb + j, G - 1));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = __ldg(wp + (int64_t)min(kb + j, G - 1) * p.NB);
+        };
         bool ok = true;
-        int i = 0;
+        int b = 0;
+        uint32_t bp = 0;
+        open(blockIdx.x);
+        load(0);
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-            float acc[128];
+            float acc[HW];
 #pragma unroll
-            for (int t = 0; t < 128; ++t) acc[t] = 0.0f;
-            for (int kb = 0; kb < G; ++kb, ++i) {
-                const int b = i & 1, s = i % SC;
-                ok = all_wait(&sfull[s], (i / SC) & 1);
-                if (!ok) break;
-                const float sc = scales[s * 256 + half * 128 + r];
-                ok = all_wait(&dfull[b], (i >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
+            for (int t = 0; t < HW; ++t) acc[t] = 0.0f;
+            for (int k0 = 0; k0 < G && ok; k0 += 4) {
+                float sc[4];
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(lanes + b * 256 + c, v);
-                    tmem_ld_wait();
-                    if (c == 96) {
+                for (int j = 0; j < 4; ++j) sc[j] = row >= 0 ? __fmul_rn(x[j], w[j]) : 0.0f;
+                if (k0 + 4 < G) load(k0 + 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (k0 + j >= G || !ok) break;
+                    ok = all_wait(&dfull[b], bp);
+                    if (!ok) break;
+                    tc_fence_after();
+                    fp8_fold<HW, false>(acc, lanes + b * BN, nullptr, sc[j], [&]() {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&dempty[b]);
-                            mbar_arrive(&sempty[s]);
-                        }
-                    }
-#pragma unroll
-                    for (int t = 0; t < 32; ++t) acc[c + t] = fmaf(__uint_as_float(v[t]), sc, acc[c + t]);
+                        if (lane == 0) mbar_arrive(&dempty[b]);
+                    });
+                    if (++b == DB) { b = 0; bp ^= 1; }
                 }
             }
             if (!ok) break;
-            walk.at(tile);
-            const int slot = walk.first() + r, n0 = walk.slab * 256 + half * 128;
-            if (r < walk.rows()) {
-                const bool zero = fp8_row(p, slot) < 0;
-                uint16_t* y = p.Y + (int64_t)slot * p.N + n0;
+            // Y: 32 x 32 blocks turned in shared memory, so that four lanes store 64 bytes of a row
+            const bool zero = row < 0;
+            const int os0 = s0, orows = rows, on0 = n0;
+            if (tile + (int)gridDim.x < tiles) {
+                open(tile + gridDim.x);
+                load(0);
+            }
 #pragma unroll
-                for (int c = 0; c < 128; c += 8) {
-                    if (n0 + c < p.N) {
-                        uint4 v = make_uint4(fp8_out2(p, acc[c], acc[c + 1]), fp8_out2(p, acc[c + 2], acc[c + 3]),
-                                             fp8_out2(p, acc[c + 4], acc[c + 5]), fp8_out2(p, acc[c + 6], acc[c + 7]));
-                        if (zero) v = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4*>(y + c) = v;
-                    }
+            for (int c = 0; c < HW; c += 32) {
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) o[t] = zero ? 0u : fp8_out2(p, acc[c + 8 * j + 2 * t], acc[c + 8 * j + 2 * t + 1]);
+                    *reinterpret_cast<uint4*>(out + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                __syncwarp();
+                const int n = on0 + c + 8 * (lane & 3);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 8 * j + (lane >> 2);
+                    const uint4 v = *reinterpret_cast<const uint4*>(out + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+                    if (r < orows && n < p.N) *reinterpret_cast<uint4*>(p.Y + (int64_t)(os0 + r) * p.N + n) = v;
                 }
             }
         }
@@ -735,7 +869,7 @@ __global__ void __launch_bounds__(Fp8TileCfg::THREADS, 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::TMEM_COLS);
+        tmem_dealloc(tmem, C::DB * BN);
     }
 }
 

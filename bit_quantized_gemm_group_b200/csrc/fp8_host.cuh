@@ -44,7 +44,7 @@ struct Fp8Workspace {
 Fp8Workspace fp8_stream_workspace(int nt)
 {
     const size_t grid = num_sms(), c = (grid * 8 + 255) / 256 * 256;
-    return {c, c + grid * 2 * nt * 128 * sizeof(float)};
+    return {c, c + grid * 2 * nt * 256 * sizeof(float)};
 }
 
 // A size that serves every number of experts, for the experts' product.
@@ -55,7 +55,7 @@ size_t fp8_workspace(int M, bool experts)
 }
 
 // The weights as {N, K, E} (boxes of 128 columns x 128 k), the activations as {K, Mx}
-// (boxes of 128 k x `box` rows; 1: gathered).
+// (boxes of 128 k x `box` rows, or of one row to be gathered).
 qg_status fp8_maps(CUtensorMap* tw, CUtensorMap* tx, const uint8_t* Xq, const uint8_t* Wq, const qg::Fp8Params& p, int box)
 {
     const uint64_t N = p.N, K = p.K;
@@ -82,23 +82,24 @@ qg_status launch_fp8_stream(qg::Fp8Params p, const uint8_t* Xq, const uint8_t* W
     do p.token = next_decode_token() << 8;
     while (p.token == 0);
     int grid = num_sms();
-    if (!p.offsets) grid = (int)std::min<int64_t>(grid, (int64_t)((p.S + NT - 1) / NT) * ((p.N + 127) / 128) * p.G);
+    if (!p.offsets) grid = (int)std::min<int64_t>(grid, (int64_t)((p.S + NT - 1) / NT) * ((p.N + 255) / 256) * p.G);
     return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::TOTAL, stream, p, tw, tx);
 }
 
+template <int BN>
 qg_status launch_fp8_tile(const qg::Fp8Params& p, const uint8_t* Xq, const uint8_t* Wq, qg_stream_t stream)
 {
-    using C = qg::Fp8TileCfg;
-    auto kern = qg::fp8_tile_kernel;
+    using C = qg::Fp8TileCfg<BN>;
+    auto kern = qg::fp8_tile_kernel<BN>;
     static KernelInfo info;
     int occ = 1;
     qg_status st = prepare_kernel(info, kern, C::THREADS, C::TOTAL, &occ);
     if (st != QG_OK) return st;
     CUtensorMap tw, tx;
-    if ((st = fp8_maps(&tw, &tx, Xq, Wq, p, C::BM)) != QG_OK) return st;
+    if ((st = fp8_maps(&tw, &tx, Xq, Wq, p, 128)) != QG_OK) return st;
     // at most so many tiles: every expert may end inside one
     const int64_t rows = (int64_t)(p.S + C::BM - 1) / C::BM + (p.offsets ? std::min(p.S, p.E) : 0);
-    const int grid = (int)std::min<int64_t>(num_sms(), rows * ((p.N + C::BN - 1) / C::BN));
+    const int grid = (int)std::min<int64_t>(num_sms(), rows * ((p.N + BN - 1) / BN));
     kern<<<grid, C::THREADS, C::TOTAL, reinterpret_cast<cudaStream_t>(stream)>>>(p, tw, tx);
     QG_CUDA(cudaGetLastError());
     return QG_OK;
@@ -134,8 +135,12 @@ qg_status fp8_gemm(const uint8_t* Xq, const float* xs, int Mx, int K, const int3
         case 32: return launch_fp8_stream<32>(p, Xq, Wq, workspace, stream);
         case 64: return launch_fp8_stream<64>(p, Xq, Wq, workspace, stream);
         case 128: return launch_fp8_stream<128>(p, Xq, Wq, workspace, stream);
-        default: return launch_fp8_tile(p, Xq, Wq, stream);
+        default: break;
     }
+    // 256 columns a tile where the tiles then still fill the GPU
+    const int64_t m_tiles = (int64_t)(S + 127) / 128 + (offsets ? std::min(S, E) / 2 : 0);
+    if (m_tiles * ((N + 255) / 256) < num_sms()) return launch_fp8_tile<128>(p, Xq, Wq, stream);
+    return launch_fp8_tile<256>(p, Xq, Wq, stream);
 }
 
 // ---------------------------------------------------------------------------
