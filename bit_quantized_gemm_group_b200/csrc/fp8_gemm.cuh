@@ -21,6 +21,8 @@
 // Every wait is bounded (mbar_wait); one that gives up records QG_ERR_TIMEOUT, and the role
 // stops issuing, waits for its own copies and MMAs, and leaves.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 #include "fp8_quant.cuh"
 
@@ -66,6 +68,16 @@ QG_DEV_INLINE void tma_gather4(const CUtensorMap* m, uint64_t* bar, void* smem_d
         "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
         "[%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+        : "memory");
+}
+
+// `bytes` (a multiple of 16, both ends 16-byte aligned) from global to shared memory
+QG_DEV_INLINE void bulk_load(uint64_t* bar, void* smem_dst, const void* src, uint32_t bytes)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            smem_u32(smem_dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -201,8 +213,8 @@ QG_DEV_INLINE void fp8_gather_rows(const Fp8Params& p, int s0, int rows, int lan
     }
 }
 
-QG_DEV_INLINE uint16_t fp8_out(const Fp8Params& p, float v) { return p.bf16 ? f32_to_bf16_bits(v) : f32_to_f16_bits(v); }
-QG_DEV_INLINE uint32_t fp8_out2(const Fp8Params& p, float a, float b) { return p.bf16 ? pack_bf16x2_rn(a, b) : pack_f16x2_rn(a, b); }
+template <bool BF16>
+QG_DEV_INLINE uint32_t fp8_out2(float a, float b) { return BF16 ? pack_bf16x2_rn(a, b) : pack_f16x2_rn(a, b); }
 
 // The scales of a run of units (tiles of T rows x 256 columns), four groups at a time: a lane holds R rows, the four groups in
 // use and, loading, the four after them, so that a load has four units' time to arrive.  (One
@@ -621,18 +633,23 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, 1)
                     const int t = lane + 32 * r;
                     zero[r] = p.rows ? __ballot_sync(0xffffffffu, t < rows && fp8_row(p, s0 + t) < 0) : 0u;
                 }
-                // lane pairs exchange, so that a lane stores two adjacent columns of a row
-                const int odd = lane & 1;
-                uint16_t* y = p.Y + (int64_t)(s0 + odd) * p.N + n - odd;
+                auto store = [&](auto bf) {
+                    // lane pairs exchange, so that a lane stores two adjacent columns of a row
+                    const int odd = lane & 1;
+                    uint16_t* y = p.Y + (int64_t)(s0 + odd) * p.N + n - odd;
 #pragma unroll
-                for (int t = 0; t < NT; t += 2) {
-                    uint32_t a = fp8_out(p, acc[t]), b = fp8_out(p, acc[t + 1]);
-                    if (zero[t / 32] >> (t & 31) & 1u) a = 0;
-                    if (zero[t / 32] >> ((t + 1) & 31) & 1u) b = 0;
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                    if (t + odd < rows && n < p.N)
-                        *reinterpret_cast<uint32_t*>(y + (int64_t)t * p.N) = odd ? got | b << 16 : a | got << 16;
-                }
+                    for (int t = 0; t < NT; t += 2) {
+                        if ((t & ~15) >= rows) break;
+                        uint32_t ab = fp8_out2<decltype(bf)::value>(acc[t], acc[t + 1]);   // two rows of a column
+                        if (zero[t / 32] >> (t & 31) & 1u) ab &= 0xFFFF0000u;
+                        if (zero[t / 32] >> ((t + 1) & 31) & 1u) ab &= 0xFFFFu;
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, ab, 1);
+                        if (t + odd < rows && n < p.N)
+                            *reinterpret_cast<uint32_t*>(y + (int64_t)t * p.N) = odd ? prmt(got, ab, 0x7632) : prmt(ab, got, 0x5410);
+                    }
+                };
+                if (p.bf16) store(std::true_type{});
+                else store(std::false_type{});
             }
             kb = 0;
             walk.next();
@@ -648,11 +665,57 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
+// The tile kernel's operands: xt[tile of 128 slots][g][row], and (a map given) the rows
+// themselves in slot order.  One CTA per tile and eight groups; a wrong map entry leaves zeros.
+// ---------------------------------------------------------------------------
+constexpr int kFp8Chunk = 8;   // groups of K in a chunk of scales
+
+__global__ void __launch_bounds__(256) fp8_rows_kernel(const Fp8Params p, const uint8_t* __restrict__ Xq,
+                                                       float* __restrict__ xt, uint8_t* __restrict__ xg)
+{
+    __shared__ Fp8Sched sched;
+    __shared__ int row[128];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!fp8_schedule<128>(sched, p, 1)) return;
+    const int mt = blockIdx.x, g0 = blockIdx.y * kFp8Chunk;
+    if (mt >= sched.pre[p.E]) return;
+    Fp8Walk<128> walk(sched, p.E, 1);
+    walk.at(mt);
+    const int s0 = walk.first(), rows = walk.rows();
+    if (threadIdx.x < 128) {
+        const int r = (int)threadIdx.x < rows ? fp8_row(p, s0 + threadIdx.x) : -2;
+        if (r == -1) set_status(6u);
+        row[threadIdx.x] = r;
+    }
+    __syncthreads();
+    float* o = xt + ((int64_t)mt * p.G + g0) * 128;
+    for (int i = threadIdx.x; i < kFp8Chunk * 128; i += 256) {
+        const int r = row[i & 127], g = g0 + (i >> 7);
+        if (g < p.G) o[i] = r >= 0 ? __ldg(p.xs + (int64_t)r * p.G + g) : 0.0f;
+    }
+    if (!xg) return;
+    const int k0 = g0 * 128, pieces = min(p.K - k0, kFp8Chunk * 128) / 16;   // 16 bytes each
+    for (int t = threadIdx.x >> 6; t < rows; t += 4) {
+        const int c = threadIdx.x & 63;
+        if (c >= pieces) continue;
+        const int r = row[t];
+        reinterpret_cast<uint4*>(xg + (int64_t)(s0 + t) * p.K + k0)[c] =
+            r >= 0 ? __ldg(reinterpret_cast<const uint4*>(Xq + (int64_t)r * p.K + k0) + c) : make_uint4(0, 0, 0, 0);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Many rows: 128 rows x BN columns, one group of K a step, persistent.
+//
+// fp8_rows_kernel before it turns the scales, so that a chunk of them is one bulk copy (loaded
+// by the folding threads, row by row or turned, they cost a tenth to a third of the time), and
+// gathers mapped rows (TMA's gather of four rows an instruction took three times as long as a
+// step's MMAs).
 //
 // Roles: warp 0 TMA; warps 1 and 3 issue the MMAs, step by step into DB buffers; warps 4..11
 // fold: thread = row, BN / 2 columns, whose weight scale is one number, so a step costs a thread
-// one scale (which it loads itself) and BN / 2 fma.
+// one scale and BN / 2 fma.
 // ---------------------------------------------------------------------------
 template <int BN>
 struct Fp8TileCfg {
@@ -661,9 +724,10 @@ struct Fp8TileCfg {
     static constexpr int ST = BN == 256 ? 4 : 6;
     static constexpr int THREADS = 384;
     static constexpr int OUT_OFF = ST * STAGE;            // per fold warp: 32 rows x 32 columns of Y
-    static constexpr int SCHED_OFF = OUT_OFF + 8 * 32 * 64;
+    static constexpr int SC_OFF = OUT_OFF + 8 * 32 * 64;  // two chunks of scales [kFp8Chunk][128]
+    static constexpr int SCHED_OFF = SC_OFF + 2 * kFp8Chunk * 128 * 4;
     static constexpr int BAR_OFF = SCHED_OFF + (int)((sizeof(Fp8Sched) + 15) / 16 * 16);
-    static constexpr int NBAR = 2 * ST + 2 * DB + 2;
+    static constexpr int NBAR = 2 * ST + 2 * DB + 4 + 2;
     static constexpr int TOTAL = BAR_OFF + NBAR * 8 + 16 + 1024;
     static_assert(TOTAL <= 227 * 1024 && ST % 2 == 0, "tile kernel shared memory");
 };
@@ -681,7 +745,10 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
     uint64_t* empty = full + ST;
     uint64_t* dfull = empty + ST;
     uint64_t* dempty = dfull + DB;
-    uint64_t* done = dempty + DB;
+    uint64_t* sfull = dempty + DB;    // chunks of scales
+    uint64_t* sempty = sfull + 2;
+    uint64_t* done = sempty + 2;
+    float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 2);
 
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -690,6 +757,10 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&sempty[i], 8);
         }
         for (int i = 0; i < DB; ++i) {
             mbar_init(&dfull[i], 1);
@@ -701,6 +772,7 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
         tma_prefetch_desc(&tm_w);
         tma_prefetch_desc(&tm_x);
     }
+    if (p.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!fp8_schedule<C::BM>(sched, p, slabs)) return;
     const int tiles = sched.pre[p.E];
     if ((int)blockIdx.x >= tiles) return;
@@ -718,30 +790,47 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
         setmaxnreg_dec<72>();
         if (warp == 0) {
             // ---------------- producer ----------------
-            int i = 0, y[4];
             const bool one = elect_one();
             bool ok = true;
+            int64_t issued = 0, chunks = 0;
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            int s = 0, sc = 0;
+            uint32_t sp = 1, scp = 1;   // parities
             for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
                 walk.at(tile);
                 const int s0 = walk.first(), n0 = walk.slab * BN;
-                if (p.rows) fp8_gather_rows(p, s0, walk.rows(), lane, y);
-                for (int kb = 0; kb < G; ++kb, ++i) {
-                    const int s = i % ST;
-                    ok = all_wait(&empty[s], ((i / ST) & 1) ^ 1);
+                const float* xt = p.xs + (int64_t)(sched.pre[walk.e] / slabs + walk.chunk) * G * 128;
+                for (int kb = 0; kb < G; ++kb) {
+                    if (kb % kFp8Chunk == 0) {
+                        ok = all_wait(&sempty[sc], scp);
+                        if (!ok) break;
+                        if (one) {
+                            const uint32_t bytes = min(kFp8Chunk, G - kb) * 512;
+                            mbar_arrive_expect_tx(&sfull[sc], bytes);
+                            bulk_load(&sfull[sc], scales + sc * kFp8Chunk * 128, xt + kb * 128, bytes);
+                        }
+                        __syncwarp();
+                        if (++sc == 2) { sc = 0; scp ^= 1; }
+                        ++chunks;
+                    }
+                    ok = all_wait(&empty[s], sp);
                     if (!ok) break;
                     uint8_t* st = smem + s * C::STAGE;
                     if (one) {
                         mbar_arrive_expect_tx(&full[s], C::STAGE);
                         tma_load_3d(&tm_w, &full[s], st + C::A_BYTES, n0, kb * 128, walk.e);
                         if (BN == 256) tma_load_3d(&tm_w, &full[s], st + C::A_BYTES + 16384, n0 + 128, kb * 128, walk.e);
-                        if (!p.rows) tma_load_2d(&tm_x, &full[s], st, kb * 128, s0);
+                        tma_load_2d(&tm_x, &full[s], st, kb * 128, s0);
                     }
                     __syncwarp();
-                    if (p.rows) tma_gather4(&tm_x, &full[s], st + lane * 512, kb * 128, y);
+                    if (++s == ST) { s = 0; sp ^= 1; }
+                    ++issued;
                 }
             }
-            if (!ok)   // copies in flight land before the block leaves
-                for (int j = max(i - ST, 0); j < i; ++j) all_wait(&full[j % ST], (j / ST) & 1);
+            if (!ok) {   // copies in flight land before the block leaves
+                for (int64_t j = issued > ST ? issued - ST : 0; j < issued; ++j) all_wait(&full[j % ST], (int)(j / ST) & 1);
+                for (int64_t j = chunks > 2 ? chunks - 2 : 0; j < chunks; ++j) all_wait(&sfull[j & 1], (int)(j >> 1) & 1);
+            }
         } else if (warp & 1) {
             // ------- MMA issuers: warp 1 the even units, warp 3 the odd ones, so that one's waits
             // lie beside the other's MMAs -------
@@ -781,87 +870,74 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + half * HW;
         uint8_t* out = smem + C::OUT_OFF + (warp - 4) * 2048;
-        const bool vec = G % 4 == 0;   // then every row of xs starts on 16 bytes
-        // the scales of this thread's row and columns, four groups at a time, the next four loading
-        float x[4], w[4];
-        int s0, rows, n0, row;
-        const float *xp, *wp;
-        auto open = [&](int tile) {
-            walk.at(tile);
-            s0 = walk.first() + 32 * q;
-            rows = walk.rows() - 32 * q;
-            n0 = walk.slab * BN + half * HW;
-            row = lane < rows ? fp8_row(p, s0 + lane) : -2;
-            if (row == -1 && walk.slab == 0 && half == 0) set_status(6u);
-            xp = p.xs + (int64_t)max(row, 0) * G;
-            wp = p.ws + (int64_t)walk.e * G * p.NB + min(n0 / 128, p.NB - 1);
-        };
-        auto load = [&](int kb) {
-            if (vec) {
-                const float4 v = __ldg(reinterpret_cast<const float4*>(xp + kb));
-                x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = __ldg(xp + min(kb + j, G - 1));
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = __ldg(wp + (int64_t)min(kb + j, G - 1) * p.NB);
-        };
         bool ok = true;
-        int b = 0;
-        uint32_t bp = 0;
-        open(blockIdx.x);
-        load(0);
+        int b = 0, sc = 0;
+        uint32_t bp = 0, scp = 0;
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // Y follows the kernel before
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
             float acc[HW];
 #pragma unroll
             for (int t = 0; t < HW; ++t) acc[t] = 0.0f;
-            for (int k0 = 0; k0 < G && ok; k0 += 4) {
-                float sc[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sc[j] = row >= 0 ? __fmul_rn(x[j], w[j]) : 0.0f;
-                if (k0 + 4 < G) load(k0 + 4);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (k0 + j >= G || !ok) break;
-                    ok = all_wait(&dfull[b], bp);
-                    if (!ok) break;
-                    tc_fence_after();
-                    fp8_fold<HW, false>(acc, lanes + b * BN, nullptr, sc[j], [&]() {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&dempty[b]);
-                    });
-                    if (++b == DB) { b = 0; bp ^= 1; }
+            // the weight scales of 32 groups, one a lane, and the next 32, loading
+            walk.at(tile);
+            const float* wp = p.ws + (int64_t)walk.e * G * p.NB + min((walk.slab * BN + half * HW) / 128, p.NB - 1);
+            float w = 0.0f, wn = lane < G ? __ldg(wp + (int64_t)lane * p.NB) : 0.0f;
+            const float* sv = nullptr;
+#pragma unroll 2
+            for (int kb = 0; kb < G; ++kb) {
+                if ((kb & 31) == 0) {
+                    w = wn;
+                    wn = kb + 32 + lane < G ? __ldg(wp + (int64_t)(kb + 32 + lane) * p.NB) : 0.0f;
                 }
+                if (kb % kFp8Chunk == 0) {
+                    ok = all_wait(&sfull[sc], scp);
+                    if (!ok) break;
+                    sv = scales + sc * kFp8Chunk * 128 + 32 * q + lane;
+                }
+                const float s = __fmul_rn(*sv, __shfl_sync(0xffffffffu, w, kb & 31));
+                sv += 128;
+                ok = all_wait(&dfull[b], bp);
+                if (!ok) break;
+                tc_fence_after();
+                fp8_fold<HW, false>(acc, lanes + b * BN, nullptr, s, [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&dempty[b]);
+                });
+                if (kb % kFp8Chunk == kFp8Chunk - 1 || kb == G - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sempty[sc]);
+                    if (++sc == 2) { sc = 0; scp ^= 1; }
+                }
+                if (++b == DB) { b = 0; bp ^= 1; }
             }
             if (!ok) break;
             // Y: 32 x 32 blocks turned in shared memory, so that four lanes store 64 bytes of a row
-            const bool zero = row < 0;
-            const int os0 = s0, orows = rows, on0 = n0;
-            if (tile + (int)gridDim.x < tiles) {
-                open(tile + gridDim.x);
-                load(0);
-            }
+            const int s0 = walk.first() + 32 * q, rows = walk.rows() - 32 * q, n0 = walk.slab * BN + half * HW;
+            auto store = [&](auto bf) {
 #pragma unroll
-            for (int c = 0; c < HW; c += 32) {
-                __syncwarp();
+                for (int c = 0; c < HW; c += 32) {
+                    __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t o[4];
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t o[4];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) o[t] = zero ? 0u : fp8_out2(p, acc[c + 8 * j + 2 * t], acc[c + 8 * j + 2 * t + 1]);
-                    *reinterpret_cast<uint4*>(out + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        for (int t = 0; t < 4; ++t)
+                            o[t] = fp8_out2<decltype(bf)::value>(acc[c + 8 * j + 2 * t], acc[c + 8 * j + 2 * t + 1]);
+                        *reinterpret_cast<uint4*>(out + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    __syncwarp();
+                    const int n = n0 + c + 8 * (lane & 3);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = 8 * j + (lane >> 2);
+                        const uint4 v = *reinterpret_cast<const uint4*>(out + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+                        if (r < rows && n < p.N) *reinterpret_cast<uint4*>(p.Y + (int64_t)(s0 + r) * p.N + n) = v;
+                    }
                 }
-                __syncwarp();
-                const int n = on0 + c + 8 * (lane & 3);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = 8 * j + (lane >> 2);
-                    const uint4 v = *reinterpret_cast<const uint4*>(out + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-                    if (r < orows && n < p.N) *reinterpret_cast<uint4*>(p.Y + (int64_t)(os0 + r) * p.N + n) = v;
-                }
-            }
+            };
+            if (p.bf16) store(std::true_type{});
+            else store(std::false_type{});
         }
     }
 

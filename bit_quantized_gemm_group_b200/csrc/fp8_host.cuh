@@ -38,7 +38,7 @@ bool fp8_bad_shape(int K, int N) { return K < 16 || K % 16 || N < 16 || N % 16; 
 int fp8_stream_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 256 ? 128 : 0; }
 
 struct Fp8Workspace {
-    size_t counters, bytes;
+    size_t first, bytes;   // the first part's, and all
 };
 
 Fp8Workspace fp8_stream_workspace(int nt)
@@ -47,11 +47,21 @@ Fp8Workspace fp8_stream_workspace(int nt)
     return {c, c + grid * 2 * nt * 256 * sizeof(float)};
 }
 
-// A size that serves every number of experts, for the experts' product.
-size_t fp8_workspace(int M, bool experts)
+// The tile kernel's operands: scales by tile and group, then (experts) the rows in slot order.
+Fp8Workspace fp8_tile_workspace(int S, int K, bool experts)
 {
-    const int nt = experts && M > 64 ? 128 : fp8_stream_rows(M);
-    return nt ? fp8_stream_workspace(nt).bytes : 0;
+    // every expert may end inside a tile of 128 rows
+    const size_t tiles = ((size_t)S + 127) / 128 + (experts ? std::min(S, qg::kFp8MaxE) : 0);
+    const size_t c = tiles * 512 * ((K + 127) / 128);
+    return {c, c + (experts ? (size_t)S * K : 0)};
+}
+
+// A size that serves every number of experts, for the experts' product.
+size_t fp8_workspace(int S, int K, bool experts)
+{
+    const int nt = experts && S > 64 ? 128 : fp8_stream_rows(S);
+    const size_t stream = nt ? fp8_stream_workspace(nt).bytes : 0;
+    return fp8_stream_rows(S) ? stream : std::max(stream, fp8_tile_workspace(S, K, experts).bytes);
 }
 
 // The weights as {N, K, E} (boxes of 128 columns x 128 k), the activations as {K, Mx}
@@ -78,7 +88,7 @@ qg_status launch_fp8_stream(qg::Fp8Params p, const uint8_t* Xq, const uint8_t* W
     CUtensorMap tw, tx;
     if ((st = fp8_maps(&tw, &tx, Xq, Wq, p, NT)) != QG_OK) return st;
     p.counters = static_cast<unsigned long long*>(ws);
-    p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + fp8_stream_workspace(NT).counters);
+    p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + fp8_stream_workspace(NT).first);
     do p.token = next_decode_token() << 8;
     while (p.token == 0);
     int grid = num_sms();
@@ -87,7 +97,7 @@ qg_status launch_fp8_stream(qg::Fp8Params p, const uint8_t* Xq, const uint8_t* W
 }
 
 template <int BN>
-qg_status launch_fp8_tile(const qg::Fp8Params& p, const uint8_t* Xq, const uint8_t* Wq, qg_stream_t stream)
+qg_status launch_fp8_tile(qg::Fp8Params p, const uint8_t* Xq, const uint8_t* Wq, void* ws, qg_stream_t stream)
 {
     using C = qg::Fp8TileCfg<BN>;
     auto kern = qg::fp8_tile_kernel<BN>;
@@ -95,14 +105,21 @@ qg_status launch_fp8_tile(const qg::Fp8Params& p, const uint8_t* Xq, const uint8
     int occ = 1;
     qg_status st = prepare_kernel(info, kern, C::THREADS, C::TOTAL, &occ);
     if (st != QG_OK) return st;
-    CUtensorMap tw, tx;
-    if ((st = fp8_maps(&tw, &tx, Xq, Wq, p, 128)) != QG_OK) return st;
+    float* xt = static_cast<float*>(ws);
+    uint8_t* xg = p.rows ? static_cast<uint8_t*>(ws) + fp8_tile_workspace(p.S, p.K, true).first : nullptr;
     // at most so many tiles: every expert may end inside one
     const int64_t rows = (int64_t)(p.S + C::BM - 1) / C::BM + (p.offsets ? std::min(p.S, p.E) : 0);
+    const dim3 chunks((unsigned)rows, (p.G + qg::kFp8Chunk - 1) / qg::kFp8Chunk);
+    if ((st = launch_pdl(qg::fp8_rows_kernel, chunks, dim3(256), 0, stream, p, Xq, xt, xg)) != QG_OK) return st;
+    p.xs = xt;
+    if (xg) {
+        p.rows = nullptr;
+        p.Mx = p.S;
+    }
+    CUtensorMap tw, tx;
+    if ((st = fp8_maps(&tw, &tx, xg ? xg : Xq, Wq, p, 128)) != QG_OK) return st;
     const int grid = (int)std::min<int64_t>(num_sms(), rows * ((p.N + BN - 1) / BN));
-    kern<<<grid, C::THREADS, C::TOTAL, reinterpret_cast<cudaStream_t>(stream)>>>(p, tw, tx);
-    QG_CUDA(cudaGetLastError());
-    return QG_OK;
+    return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::TOTAL, stream, p, tw, tx);
 }
 
 qg_status fp8_gemm(const uint8_t* Xq, const float* xs, int Mx, int K, const int32_t* rows, const int32_t* offsets, int S,
@@ -113,7 +130,7 @@ qg_status fp8_gemm(const uint8_t* Xq, const float* xs, int Mx, int K, const int3
     if (misaligned(Xq) || misaligned(xs) || misaligned(rows) || misaligned(offsets) || misaligned(Wq) ||
         misaligned(ws) || misaligned(Y) || misaligned(workspace))
         return QG_ERR_ALIGN;
-    const size_t need = fp8_workspace(S, offsets != nullptr);
+    const size_t need = fp8_workspace(S, K, offsets != nullptr);
     if (need && !workspace) return QG_ERR_NULL;
     if (need > ws_bytes) return QG_ERR_WORKSPACE;
     qg::Fp8Params p{};
@@ -139,8 +156,8 @@ qg_status fp8_gemm(const uint8_t* Xq, const float* xs, int Mx, int K, const int3
     }
     // 256 columns a tile where the tiles then still fill the GPU
     const int64_t m_tiles = (int64_t)(S + 127) / 128 + (offsets ? std::min(S, E) / 2 : 0);
-    if (m_tiles * ((N + 255) / 256) < num_sms()) return launch_fp8_tile<128>(p, Xq, Wq, stream);
-    return launch_fp8_tile<256>(p, Xq, Wq, stream);
+    if (m_tiles * ((N + 255) / 256) < num_sms()) return launch_fp8_tile<128>(p, Xq, Wq, workspace, stream);
+    return launch_fp8_tile<256>(p, Xq, Wq, workspace, stream);
 }
 
 // ---------------------------------------------------------------------------

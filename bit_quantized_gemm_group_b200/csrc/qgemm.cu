@@ -899,8 +899,8 @@ size_t qg_workspace_size(qg_op op, int M, int K, int N)
         if (M < 1 || K < 8 || K % 8 || K > 16384 || N < 1) return 0;
         return std::max(gptq_carve(nullptr, K, N).bytes, gptq_blocked_carve(nullptr, M, K, N).bytes);
     }
-    if (op == QG_OP_GEMM_FP8) return M < 1 || fp8_bad_shape(K, N) ? 0 : fp8_workspace(M, false);
-    if (op == QG_OP_GEMM_FP8_EXPERTS) return M < 1 || fp8_bad_shape(K, N) ? 0 : fp8_workspace(M, true);
+    if (op == QG_OP_GEMM_FP8) return M < 1 || fp8_bad_shape(K, N) ? 0 : fp8_workspace(M, K, false);
+    if (op == QG_OP_GEMM_FP8_EXPERTS) return M < 1 || fp8_bad_shape(K, N) ? 0 : fp8_workspace(M, K, true);
     if (op == QG_OP_EXPERT_SLOTS) return M < 1 || slots_bad_shape(M, K, N) ? 0 : slots_workspace(M, K, N);
     if (M < 1 || K < 128 || N < 8 || K % 128) return 0;
     switch (op) {
