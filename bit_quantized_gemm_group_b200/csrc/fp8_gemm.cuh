@@ -71,16 +71,6 @@ QG_DEV_INLINE void tma_gather4(const CUtensorMap* m, uint64_t* bar, void* smem_d
         : "memory");
 }
 
-// `bytes` (a multiple of 16, both ends 16-byte aligned) from global to shared memory
-QG_DEV_INLINE void bulk_load(uint64_t* bar, void* smem_dst, const void* src, uint32_t bytes)
-{
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_u32(smem_dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
-}
-
 template <int R>
 QG_DEV_INLINE void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
@@ -665,53 +655,31 @@ __global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// The tile kernel's operands: xt[tile of 128 slots][g][row], and (a map given) the rows
-// themselves in slot order.  One CTA per tile and eight groups; a wrong map entry leaves zeros.
+// The mapped rows in slot order, for the tile kernel (a wrong map entry: row 0, whose sums go
+// nowhere).  Four slots and 4 KB of K per CTA, 64 threads a slot.
 // ---------------------------------------------------------------------------
-constexpr int kFp8Chunk = 8;   // groups of K in a chunk of scales
-
 __global__ void __launch_bounds__(256) fp8_rows_kernel(const Fp8Params p, const uint8_t* __restrict__ Xq,
-                                                       float* __restrict__ xt, uint8_t* __restrict__ xg)
+                                                       uint8_t* __restrict__ xg)
 {
-    __shared__ Fp8Sched sched;
-    __shared__ int row[128];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!fp8_schedule<128>(sched, p, 1)) return;
-    const int mt = blockIdx.x, g0 = blockIdx.y * kFp8Chunk;
-    if (mt >= sched.pre[p.E]) return;
-    Fp8Walk<128> walk(sched, p.E, 1);
-    walk.at(mt);
-    const int s0 = walk.first(), rows = walk.rows();
-    if (threadIdx.x < 128) {
-        const int r = (int)threadIdx.x < rows ? fp8_row(p, s0 + threadIdx.x) : -2;
-        if (r == -1) set_status(6u);
-        row[threadIdx.x] = r;
-    }
-    __syncthreads();
-    float* o = xt + ((int64_t)mt * p.G + g0) * 128;
-    for (int i = threadIdx.x; i < kFp8Chunk * 128; i += 256) {
-        const int r = row[i & 127], g = g0 + (i >> 7);
-        if (g < p.G) o[i] = r >= 0 ? __ldg(p.xs + (int64_t)r * p.G + g) : 0.0f;
-    }
-    if (!xg) return;
-    const int k0 = g0 * 128, pieces = min(p.K - k0, kFp8Chunk * 128) / 16;   // 16 bytes each
-    for (int t = threadIdx.x >> 6; t < rows; t += 4) {
-        const int c = threadIdx.x & 63;
-        if (c >= pieces) continue;
-        const int r = row[t];
-        reinterpret_cast<uint4*>(xg + (int64_t)(s0 + t) * p.K + k0)[c] =
-            r >= 0 ? __ldg(reinterpret_cast<const uint4*>(Xq + (int64_t)r * p.K + k0) + c) : make_uint4(0, 0, 0, 0);
+    const int s = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (s >= min(p.offsets[p.E], p.S)) return;
+    const uint4* src = reinterpret_cast<const uint4*>(Xq + (int64_t)max(fp8_row(p, s), 0) * p.K);
+    uint4* dst = reinterpret_cast<uint4*>(xg + (int64_t)s * p.K);
+    const int end = min(p.K / 16, ((int)blockIdx.y + 1) * 256);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int k = blockIdx.y * 256 + i * 64 + (threadIdx.x & 63);
+        if (k < end) dst[k] = __ldg(src + k);
     }
 }
 
 // ---------------------------------------------------------------------------
 // Many rows: 128 rows x BN columns, one group of K a step, persistent.
 //
-// fp8_rows_kernel before it turns the scales, so that a chunk of them is one bulk copy (loaded
-// by the folding threads, row by row or turned, they cost a tenth to a third of the time), and
-// gathers mapped rows (TMA's gather of four rows an instruction took three times as long as a
-// step's MMAs).
+// Mapped rows are gathered by fp8_rows_kernel before it (TMA's gather of four rows an
+// instruction took three times as long as a step's MMAs).
 //
 // Roles: warp 0 TMA; warps 1 and 3 issue the MMAs, step by step into DB buffers; warps 4..11
 // fold: thread = row, BN / 2 columns, whose weight scale is one number, so a step costs a thread
@@ -724,10 +692,9 @@ struct Fp8TileCfg {
     static constexpr int ST = BN == 256 ? 4 : 6;
     static constexpr int THREADS = 384;
     static constexpr int OUT_OFF = ST * STAGE;            // per fold warp: 32 rows x 32 columns of Y
-    static constexpr int SC_OFF = OUT_OFF + 8 * 32 * 64;  // two chunks of scales [kFp8Chunk][128]
-    static constexpr int SCHED_OFF = SC_OFF + 2 * kFp8Chunk * 128 * 4;
+    static constexpr int SCHED_OFF = OUT_OFF + 8 * 32 * 64;
     static constexpr int BAR_OFF = SCHED_OFF + (int)((sizeof(Fp8Sched) + 15) / 16 * 16);
-    static constexpr int NBAR = 2 * ST + 2 * DB + 4 + 2;
+    static constexpr int NBAR = 2 * ST + 2 * DB + 2;
     static constexpr int TOTAL = BAR_OFF + NBAR * 8 + 16 + 1024;
     static_assert(TOTAL <= 227 * 1024 && ST % 2 == 0, "tile kernel shared memory");
 };
@@ -745,10 +712,7 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
     uint64_t* empty = full + ST;
     uint64_t* dfull = empty + ST;
     uint64_t* dempty = dfull + DB;
-    uint64_t* sfull = dempty + DB;    // chunks of scales
-    uint64_t* sempty = sfull + 2;
-    uint64_t* done = sempty + 2;
-    float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);
+    uint64_t* done = dempty + DB;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 2);
 
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -757,10 +721,6 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sfull[i], 1);
-            mbar_init(&sempty[i], 8);
         }
         for (int i = 0; i < DB; ++i) {
             mbar_init(&dfull[i], 1);
@@ -792,27 +752,14 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
             // ---------------- producer ----------------
             const bool one = elect_one();
             bool ok = true;
-            int64_t issued = 0, chunks = 0;
+            int64_t issued = 0;
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            int s = 0, sc = 0;
-            uint32_t sp = 1, scp = 1;   // parities
+            int s = 0;
+            uint32_t sp = 1;   // parity
             for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
                 walk.at(tile);
                 const int s0 = walk.first(), n0 = walk.slab * BN;
-                const float* xt = p.xs + (int64_t)(sched.pre[walk.e] / slabs + walk.chunk) * G * 128;
                 for (int kb = 0; kb < G; ++kb) {
-                    if (kb % kFp8Chunk == 0) {
-                        ok = all_wait(&sempty[sc], scp);
-                        if (!ok) break;
-                        if (one) {
-                            const uint32_t bytes = min(kFp8Chunk, G - kb) * 512;
-                            mbar_arrive_expect_tx(&sfull[sc], bytes);
-                            bulk_load(&sfull[sc], scales + sc * kFp8Chunk * 128, xt + kb * 128, bytes);
-                        }
-                        __syncwarp();
-                        if (++sc == 2) { sc = 0; scp ^= 1; }
-                        ++chunks;
-                    }
                     ok = all_wait(&empty[s], sp);
                     if (!ok) break;
                     uint8_t* st = smem + s * C::STAGE;
@@ -827,10 +774,8 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
                     ++issued;
                 }
             }
-            if (!ok) {   // copies in flight land before the block leaves
+            if (!ok)   // copies in flight land before the block leaves
                 for (int64_t j = issued > ST ? issued - ST : 0; j < issued; ++j) all_wait(&full[j % ST], (int)(j / ST) & 1);
-                for (int64_t j = chunks > 2 ? chunks - 2 : 0; j < chunks; ++j) all_wait(&sfull[j & 1], (int)(j >> 1) & 1);
-            }
         } else if (warp & 1) {
             // ------- MMA issuers: warp 1 the even units, warp 3 the odd ones, so that one's waits
             // lie beside the other's MMAs -------
@@ -870,50 +815,69 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + half * HW;
         uint8_t* out = smem + C::OUT_OFF + (warp - 4) * 2048;
+        const bool vec = G % 4 == 0;   // then every row of xs starts on 16 bytes
+        // the scales of this thread's row and columns, four groups at a time, the next four loading
+        float x[4], w[4];
+        int s0, rows, n0, row;
+        const float *xp, *wp;
+        auto open = [&](int tile) {
+            walk.at(tile);
+            s0 = walk.first() + 32 * q;
+            rows = walk.rows() - 32 * q;
+            n0 = walk.slab * BN + half * HW;
+            row = lane < rows ? fp8_row(p, s0 + lane) : -2;
+            if (row == -1 && walk.slab == 0 && half == 0) set_status(6u);
+            xp = p.xs + (int64_t)max(row, 0) * G;
+            wp = p.ws + (int64_t)walk.e * G * p.NB + min(n0 / 128, p.NB - 1);
+        };
+        auto load = [&](int kb) {
+            if (vec) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(xp + kb));
+                x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = __ldg(xp + min(kb + j, G - 1));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = __ldg(wp + (int64_t)min(kb + j, G - 1) * p.NB);
+        };
         bool ok = true;
-        int b = 0, sc = 0;
-        uint32_t bp = 0, scp = 0;
-        asm volatile("griddepcontrol.wait;" ::: "memory");   // Y follows the kernel before
+        int b = 0;
+        uint32_t bp = 0;
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // xs and Y follow the kernel before
+        open(blockIdx.x);
+        load(0);
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
             float acc[HW];
 #pragma unroll
             for (int t = 0; t < HW; ++t) acc[t] = 0.0f;
-            // the weight scales of 32 groups, one a lane, and the next 32, loading
-            walk.at(tile);
-            const float* wp = p.ws + (int64_t)walk.e * G * p.NB + min((walk.slab * BN + half * HW) / 128, p.NB - 1);
-            float w = 0.0f, wn = lane < G ? __ldg(wp + (int64_t)lane * p.NB) : 0.0f;
-            const float* sv = nullptr;
-#pragma unroll 2
-            for (int kb = 0; kb < G; ++kb) {
-                if ((kb & 31) == 0) {
-                    w = wn;
-                    wn = kb + 32 + lane < G ? __ldg(wp + (int64_t)(kb + 32 + lane) * p.NB) : 0.0f;
-                }
-                if (kb % kFp8Chunk == 0) {
-                    ok = all_wait(&sfull[sc], scp);
+            for (int k0 = 0; k0 < G && ok; k0 += 4) {
+                float sc[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sc[j] = row >= 0 ? __fmul_rn(x[j], w[j]) : 0.0f;
+                if (k0 + 4 < G) load(k0 + 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (k0 + j >= G || !ok) break;
+                    ok = all_wait(&dfull[b], bp);
                     if (!ok) break;
-                    sv = scales + sc * kFp8Chunk * 128 + 32 * q + lane;
+                    tc_fence_after();
+                    fp8_fold<HW, false>(acc, lanes + b * BN, nullptr, sc[j], [&]() {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&dempty[b]);
+                    });
+                    if (++b == DB) { b = 0; bp ^= 1; }
                 }
-                const float s = __fmul_rn(*sv, __shfl_sync(0xffffffffu, w, kb & 31));
-                sv += 128;
-                ok = all_wait(&dfull[b], bp);
-                if (!ok) break;
-                tc_fence_after();
-                fp8_fold<HW, false>(acc, lanes + b * BN, nullptr, s, [&]() {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&dempty[b]);
-                });
-                if (kb % kFp8Chunk == kFp8Chunk - 1 || kb == G - 1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sempty[sc]);
-                    if (++sc == 2) { sc = 0; scp ^= 1; }
-                }
-                if (++b == DB) { b = 0; bp ^= 1; }
             }
             if (!ok) break;
             // Y: 32 x 32 blocks turned in shared memory, so that four lanes store 64 bytes of a row
-            const int s0 = walk.first() + 32 * q, rows = walk.rows() - 32 * q, n0 = walk.slab * BN + half * HW;
+            const bool zero = row < 0;
+            const int os0 = s0, orows = rows, on0 = n0;
+            if (tile + (int)gridDim.x < tiles) {
+                open(tile + gridDim.x);
+                load(0);
+            }
             auto store = [&](auto bf) {
 #pragma unroll
                 for (int c = 0; c < HW; c += 32) {
@@ -923,16 +887,16 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
                         uint32_t o[4];
 #pragma unroll
                         for (int t = 0; t < 4; ++t)
-                            o[t] = fp8_out2<decltype(bf)::value>(acc[c + 8 * j + 2 * t], acc[c + 8 * j + 2 * t + 1]);
+                            o[t] = zero ? 0u : fp8_out2<decltype(bf)::value>(acc[c + 8 * j + 2 * t], acc[c + 8 * j + 2 * t + 1]);
                         *reinterpret_cast<uint4*>(out + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
                     __syncwarp();
-                    const int n = n0 + c + 8 * (lane & 3);
+                    const int n = on0 + c + 8 * (lane & 3);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int r = 8 * j + (lane >> 2);
                         const uint4 v = *reinterpret_cast<const uint4*>(out + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-                        if (r < rows && n < p.N) *reinterpret_cast<uint4*>(p.Y + (int64_t)(s0 + r) * p.N + n) = v;
+                        if (r < orows && n < p.N) *reinterpret_cast<uint4*>(p.Y + (int64_t)(os0 + r) * p.N + n) = v;
                     }
                 }
             };

@@ -47,21 +47,13 @@ Fp8Workspace fp8_stream_workspace(int nt)
     return {c, c + grid * 2 * nt * 256 * sizeof(float)};
 }
 
-// The tile kernel's operands: scales by tile and group, then (experts) the rows in slot order.
-Fp8Workspace fp8_tile_workspace(int S, int K, bool experts)
-{
-    // every expert may end inside a tile of 128 rows
-    const size_t tiles = ((size_t)S + 127) / 128 + (experts ? std::min(S, qg::kFp8MaxE) : 0);
-    const size_t c = tiles * 512 * ((K + 127) / 128);
-    return {c, c + (experts ? (size_t)S * K : 0)};
-}
-
-// A size that serves every number of experts, for the experts' product.
+// A size that serves every number of experts, for the experts' product: the stream kernel's,
+// and the tile kernel's rows in slot order.
 size_t fp8_workspace(int S, int K, bool experts)
 {
     const int nt = experts && S > 64 ? 128 : fp8_stream_rows(S);
     const size_t stream = nt ? fp8_stream_workspace(nt).bytes : 0;
-    return fp8_stream_rows(S) ? stream : std::max(stream, fp8_tile_workspace(S, K, experts).bytes);
+    return experts && !fp8_stream_rows(S) ? std::max(stream, (size_t)S * K) : stream;
 }
 
 // The weights as {N, K, E} (boxes of 128 columns x 128 k), the activations as {K, Mx}
@@ -105,19 +97,18 @@ qg_status launch_fp8_tile(qg::Fp8Params p, const uint8_t* Xq, const uint8_t* Wq,
     int occ = 1;
     qg_status st = prepare_kernel(info, kern, C::THREADS, C::TOTAL, &occ);
     if (st != QG_OK) return st;
-    float* xt = static_cast<float*>(ws);
-    uint8_t* xg = p.rows ? static_cast<uint8_t*>(ws) + fp8_tile_workspace(p.S, p.K, true).first : nullptr;
+    CUtensorMap tw, tx;
+    qg::Fp8Params x = p;   // the rows as the kernel reads them
+    if (p.rows) {
+        const dim3 g((p.S + 3) / 4, (p.K + 4095) / 4096);
+        if ((st = launch_pdl(qg::fp8_rows_kernel, g, dim3(256), 0, stream, p, Xq, static_cast<uint8_t*>(ws))) != QG_OK) return st;
+        Xq = static_cast<const uint8_t*>(ws);
+        x.rows = nullptr;
+        x.Mx = p.S;
+    }
+    if ((st = fp8_maps(&tw, &tx, Xq, Wq, x, 128)) != QG_OK) return st;
     // at most so many tiles: every expert may end inside one
     const int64_t rows = (int64_t)(p.S + C::BM - 1) / C::BM + (p.offsets ? std::min(p.S, p.E) : 0);
-    const dim3 chunks((unsigned)rows, (p.G + qg::kFp8Chunk - 1) / qg::kFp8Chunk);
-    if ((st = launch_pdl(qg::fp8_rows_kernel, chunks, dim3(256), 0, stream, p, Xq, xt, xg)) != QG_OK) return st;
-    p.xs = xt;
-    if (xg) {
-        p.rows = nullptr;
-        p.Mx = p.S;
-    }
-    CUtensorMap tw, tx;
-    if ((st = fp8_maps(&tw, &tx, xg ? xg : Xq, Wq, p, 128)) != QG_OK) return st;
     const int grid = (int)std::min<int64_t>(num_sms(), rows * ((p.N + BN - 1) / BN));
     return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::TOTAL, stream, p, tw, tx);
 }
