@@ -6,17 +6,12 @@
 // and the same per expert over the rows of its slots.  ("AI Infra guide, ch.4
 // Quantization" sec. 5, e4m3; "LLM inference cost ..." sec. 2.2, groups of 128.)
 //
-// What both kernels share.  The scales change every 128 of K, so the tensor core sums one
-// group at a time (fp32, tensor memory) and the epilogue warps fold each group's sums into
-// fp32 registers with one fma, acc += P * (xs * ws), while the tensor core works on the next
-// group in another buffer.  The weights stay as they are stored, [K][N]: a TMA box of
-// 128 k x 128 columns, 128-byte swizzle, is the MMA's MN-major operand.  A dense product is
-// the experts' product with one expert that has all the rows; rows are gathered by TMA
-// (four rows an instruction) when a map is given.
-//
-//   fp8_stream_kernel: few rows.  128 columns are the MMA's M, 16..128 rows its N; the
-//     weights are streamed once, the (tile, group) units split evenly over the CTAs.
-//   fp8_tile_kernel: many rows.  128 rows x 256 columns, persistent.
+// The scales change every 128 of K, so the tensor core sums one group at a time (fp32, tensor
+// memory) and the epilogue warps fold each group's sums into fp32 registers with one fma,
+// acc += P * (xs * ws), while the tensor core works on the next group in another buffer.  The
+// weights stay as they are stored, [K][N]: a TMA box of 128 k x 128 columns, 128-byte swizzle, is
+// the MMA's MN-major operand.  A dense product is the experts' product with one expert that has
+// all the rows.
 //
 // Every wait is bounded (mbar_wait); one that gives up records QG_ERR_TIMEOUT, and the role
 // stops issuing, waits for its own copies and MMAs, and leaves.
@@ -35,10 +30,11 @@ struct Fp8Params {
     const int32_t* offsets;  // [E + 1], or NULL: one expert with all S slots
     uint16_t* Y;             // [S][N]
     int Mx, S, E, K, N, G, NB;
+    int box;                 // rows of a TMA box of activations: what a tile can have
     bool bf16;
-    // stream kernel: the workspace
+    // the workspace of split tiles
     unsigned long long* counters;  // [grid]
-    float* partials;               // [grid][2][NT][256]
+    float* partials;               // [grid][2][128][BN]
     unsigned long long token;      // this launch's token (its low byte is 0, the rest is not)
 };
 
@@ -58,16 +54,6 @@ QG_DEV_INLINE void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accum)
-        : "memory");
-}
-
-// Four rows y[0..3] of a 2-D map whose box is one row high, to consecutive rows of the tile.
-QG_DEV_INLINE void tma_gather4(const CUtensorMap* m, uint64_t* bar, void* smem_dst, int x, const int (&y)[4])
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
         : "memory");
 }
 
@@ -170,16 +156,6 @@ struct Fp8Walk {
         slab = r / chunks;
         chunk = r - slab * chunks;
     }
-    QG_DEV_INLINE void next()
-    {
-        if (++chunk < chunks) return;
-        chunk = 0;
-        if (++slab < slabs) return;
-        slab = 0;
-        do ++e;
-        while (e < E && sc.off[e + 1] == sc.off[e]);
-        if (e < E) chunks = (sc.off[e + 1] - sc.off[e] + T - 1) / T;
-    }
     QG_DEV_INLINE int first() const { return sc.off[e] + chunk * T; }
     QG_DEV_INLINE int rows() const { return min(T, sc.off[e + 1] - first()); }
 };
@@ -192,110 +168,13 @@ QG_DEV_INLINE int fp8_row(const Fp8Params& p, int s)
     return (uint32_t)r < (uint32_t)p.Mx ? r : -1;
 }
 
-// The four rows that this lane gathers of a tile (lane l: rows 4l .. 4l + 3); rows past the
-// tile's and wrong entries read row 0, whose sums go nowhere.
-QG_DEV_INLINE void fp8_gather_rows(const Fp8Params& p, int s0, int rows, int lane, int (&y)[4])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = 4 * lane + i;
-        y[i] = t < rows ? max(fp8_row(p, s0 + t), 0) : 0;
-    }
-}
-
 template <bool BF16>
 QG_DEV_INLINE uint32_t fp8_out2(float a, float b) { return BF16 ? pack_bf16x2_rn(a, b) : pack_f16x2_rn(a, b); }
 
-// The scales of a run of units (tiles of T rows x 256 columns), four groups at a time: a lane holds R rows, the four groups in
-// use and, loading, the four after them, so that a load has four units' time to arrive.  (One
-// load per unit, four units ahead, was slower: a wait for one of them waited for all.)
-template <int T, int R>
-struct Fp8Scales {
-    const Fp8Params& p;
-    Fp8Walk<T> walk;      // of the tile being loaded
-    int64_t left;         // units not yet loaded
-    int lane, kb;         // first group not yet loaded
-    int row[R];
-    const float* wsp;     // the tile's first weight scale
-    bool wide;            // its second 128 columns exist
-    float x[R][4], w[2][4], nx[R][4], nw[2][4];
-    int n, nn;            // groups held and loading
-
-    QG_DEV_INLINE Fp8Scales(const Fp8Params& p_, const Fp8Walk<T>& w_, int64_t units, int kb0, int lane_)
-        : p(p_), walk(w_), left(units), lane(lane_), kb(kb0), n(0), nn(0)
-    {
-        tile();
-        load();
-    }
-    QG_DEV_INLINE void tile()
-    {
-        const int s0 = walk.first(), rows = walk.rows();
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int t = lane + 32 * r;
-            row[r] = t < rows ? fp8_row(p, s0 + t) : -2;
-            if (row[r] == -1) set_status(6u);
-        }
-        wsp = p.ws + (int64_t)walk.e * p.G * p.NB + 2 * walk.slab;
-        wide = 2 * walk.slab + 1 < p.NB;
-    }
-    QG_DEV_INLINE void load()
-    {
-        nn = (int)min((int64_t)min(4 - (kb & 3), p.G - kb), left);
-        if (nn == 0) return;
-        const bool vec = p.G % 4 == 0;   // then every row starts on 16 bytes
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float* src = p.xs + (int64_t)max(row[r], 0) * p.G + kb;
-            if (vec && nn == 4) {
-                const float4 v = __ldg(reinterpret_cast<const float4*>(src));
-                nx[r][0] = v.x; nx[r][1] = v.y; nx[r][2] = v.z; nx[r][3] = v.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) nx[r][j] = j < nn ? __ldg(src + j) : 0.0f;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float* src = wsp + (int64_t)(kb + j) * p.NB;
-            nw[0][j] = j < nn ? __ldg(src) : 0.0f;
-            nw[1][j] = j < nn && wide ? __ldg(src + 1) : 0.0f;
-        }
-    }
-    // The loaded groups become those in use, the next ones are requested; false: none left.
-    QG_DEV_INLINE bool advance()
-    {
-        n = nn;
-        if (n == 0) return false;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[r][j] = row[r] >= 0 ? nx[r][j] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            w[0][j] = nw[0][j];
-            w[1][j] = nw[1][j];
-        }
-        left -= n;
-        kb += n;
-        if (kb == p.G) {
-            kb = 0;
-            if (left > 0) {
-                walk.next();
-                tile();
-            }
-        }
-        load();
-        return true;
-    }
-};
-
-// acc[0 .. CW) += (CW sums of tensor memory at `addr`) * scale, where the scale of sum t is
-// sv[t] (shared memory, 16-byte aligned; PER = true) or the one number sc.  Sixteen columns at a
-// time, the next ones' load in flight while the ones before are folded; `release` runs once all
-// are read (PER: and their scales too).
-template <int CW, bool PER, typename F>
-QG_DEV_INLINE void fp8_fold(float (&acc)[CW], uint32_t addr, const float* sv, float sc, F release)
+// acc[0 .. CW) += (CW sums of tensor memory at `addr`) * sc.  Sixteen columns at a time, the next
+// ones' load in flight while the ones before are folded; `release` runs once all are read.
+template <int CW, typename F>
+QG_DEV_INLINE void fp8_fold(float (&acc)[CW], uint32_t addr, float sc, F release)
 {
     uint32_t v[2][16];
     tmem_ld_32x32b_x16(addr, v[0]);
@@ -306,351 +185,106 @@ QG_DEV_INLINE void fp8_fold(float (&acc)[CW], uint32_t addr, const float* sv, fl
 #pragma unroll
         for (int t = 0; t < 16; ++t) asm volatile("" : "+r"(u[t]));   // read only after the wait
         if (c + 16 < CW) tmem_ld_32x32b_x16(addr + c + 16, v[(c / 16 + 1) & 1]);
-        else if (!PER) release();
+        else release();
 #pragma unroll
-        for (int t = 0; t < 16; t += 4) {
-            float4 s4 = make_float4(sc, sc, sc, sc);
-            if constexpr (PER) s4 = *reinterpret_cast<const float4*>(sv + c + t);
-            acc[c + t] = fmaf(__uint_as_float(u[t]), s4.x, acc[c + t]);
-            acc[c + t + 1] = fmaf(__uint_as_float(u[t + 1]), s4.y, acc[c + t + 1]);
-            acc[c + t + 2] = fmaf(__uint_as_float(u[t + 2]), s4.z, acc[c + t + 2]);
-            acc[c + t + 3] = fmaf(__uint_as_float(u[t + 3]), s4.w, acc[c + t + 3]);
-        }
+        for (int t = 0; t < 16; ++t) acc[c + t] = fmaf(__uint_as_float(u[t]), sc, acc[c + t]);
     }
-    if (PER) release();
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: stream-K
+// Which tiles, and which groups of K, a CTA takes
 //
-// Tiles of NT rows x 256 columns (256 so that a weight row is read 256 bytes at a time: with
-// 128-byte boxes DRAM read 1.37 times the weights).  Units are (tile, group of K); CTA c takes
-// units [c U / grid, (c + 1) U / grid).  A tile whose units lie in several CTAs is joined by
-// whichever of them arrives last: each leaves its fp32 sums in the workspace and counts itself
-// in; the last one adds all of them in CTA order (the result does not depend on who is last)
-// and writes Y.  No CTA waits for another.  The counter word holds the launch's token above an
+// Whole waves of tiles go one to a CTA, `grid` apart, so that CTAs running together share
+// weights and rows.  Where the tiles left over would leave many CTAs idle, their units (tile,
+// group of K) are split evenly over all of them: CTA c takes units
+// [c U / eff, (c + 1) U / eff), at most two pieces of tiles.  A split tile is joined by whichever
+// of its CTAs arrives last: each leaves its fp32 sums in the workspace and counts itself in; the
+// last one adds all of them in CTA order (the result does not depend on who is last) and
+// writes Y.  No CTA waits for another.  The counter word holds the launch's token above an
 // 8-bit count, so whatever an unused workspace holds reads as 0, and the last arrival clears
 // it, so a replayed graph finds it so again.
-//
-// Roles: warp 0 TMA; warp 1 issues the MMAs (the 128-column halves are M, the rows N; each
-// unit into one of DB buffers); warp 2 writes the units' scales; warps 4..11 fold the units
-// (thread = column).
 // ---------------------------------------------------------------------------
-template <int NT>
-struct Fp8StreamCfg {
-    static constexpr int W_BYTES = 2 * 128 * 128, X_BYTES = NT * 128;
-    static constexpr int STAGE = W_BYTES + X_BYTES;
-    static constexpr int ST = NT <= 32 ? 6 : 4;     // even: a stage always serves the same issuer
-    static constexpr int DB = NT == 128 ? 2 : 4;    // buffers of sums [2][NT]
-    static constexpr int SC = 8;                    // slots of scales [2][NT]
-    static constexpr int EPI = 8;
-    static constexpr int THREADS = 32 * (4 + EPI);
-    static constexpr int TMEM_COLS = DB * 2 * NT;
-    static constexpr int SC_OFF = ST * STAGE;
-    static constexpr int SCHED_OFF = SC_OFF + SC * 2 * NT * 4;
-    static constexpr int BAR_OFF = SCHED_OFF + (int)((sizeof(Fp8Sched) + 15) / 16 * 16);
-    static constexpr int NBAR = 2 * ST + 2 * DB + 2 * SC + 2;
-    static constexpr int TOTAL = BAR_OFF + NBAR * 8 + 16 + 1024;
-    static constexpr int PARTIAL = NT * 256;        // floats of a piece's sums
-    static_assert(STAGE % 1024 == 0 && TOTAL <= 227 * 1024 - 64 && ST % 2 == 0, "stream kernel shared memory");
+// Splitting costs the join: about 11 us for a few rows and 20 us for 128, where a step of 128
+// columns takes 0.32 us, so the longest CTA has to save fp8_min_saved() steps.  K = 11008, N =
+// 4096, 4 rows (86 steps down to 19): 27.5 -> 17.1 us; K = 4096 (32 down to 7): 11.8 -> 13.8 us,
+// left whole; K = 11008 with 128 rows: no difference.
+constexpr int kFp8MinUnits = 4;   // of a piece
+QG_DEV_INLINE int fp8_min_saved(int rows) { return 34 + rows / 4; }
+
+struct Fp8Work {   // in shared memory: the folding threads have no registers to spare
+    int G, grid, cta;
+    int whole;       // whole tiles of this CTA: cta, cta + grid, ..
+    int base;        // the first split tile
+    int eff;         // CTAs that take units of split tiles
+    int64_t units;   // of all split tiles
+    int64_t u0;      // this CTA's: [u0, u0 + n)
+    int n;
+    QG_DEV_INLINE void init(int tiles, int rows, int G_, int grid_, int cta_)
+    {
+        G = G_;
+        grid = grid_;
+        cta = cta_;
+        base = tiles;
+        eff = n = 0;
+        units = u0 = 0;
+        const int left = tiles % grid;
+        const int parts = left ? (int)min((int64_t)grid, max((int64_t)left, (int64_t)left * G / kFp8MinUnits)) : 1;
+        if (G - (int)((int64_t)left * G / parts) >= fp8_min_saved(rows) && left > 0) {
+            whole = tiles / grid;
+            base = tiles - left;
+            units = (int64_t)left * G;
+            eff = parts;
+            if (cta < eff) {
+                u0 = first(cta);
+                n = (int)(first(cta + 1) - u0);
+            }
+        } else {
+            whole = cta < tiles ? (tiles - 1 - cta) / grid + 1 : 0;
+        }
+    }
+    QG_DEV_INLINE int64_t first(int c) const { return c * units / eff; }
+    QG_DEV_INLINE int cta_of(int64_t u) const
+    {
+        int c = (int)(u * eff / units);
+        while (c > 0 && first(c) > u) --c;
+        while (first(c + 1) <= u) ++c;
+        return c;
+    }
+    QG_DEV_INLINE int64_t steps() const { return (int64_t)whole * G + n; }
+    // Piece i: groups [k0, k1) of a tile; false: no such piece.
+    QG_DEV_INLINE bool piece(int i, int& tile, int& k0, int& k1) const
+    {
+        if (i < whole) {
+            tile = cta + i * grid;
+            k0 = 0;
+            k1 = G;
+            return true;
+        }
+        if (n == 0) return false;
+        const int t = (int)(u0 / G), k = (int)(u0 - (int64_t)t * G), len = min(n, G - k);
+        if (i == whole) {
+            tile = base + t;
+            k0 = k;
+            k1 = k + len;
+            return true;
+        }
+        tile = base + t + 1;
+        k0 = 0;
+        k1 = n - len;
+        return i == whole + 1 && k1 > 0;
+    }
 };
-
-QG_DEV_INLINE int64_t fp8_first_unit(int c, int64_t units, int grid) { return c * units / grid; }
-
-QG_DEV_INLINE int fp8_cta_of_unit(int64_t u, int64_t units, int grid)
-{
-    int c = (int)(u * grid / units);
-    while (c > 0 && fp8_first_unit(c, units, grid) > u) --c;
-    while (fp8_first_unit(c + 1, units, grid) <= u) ++c;
-    return c;
-}
 
 // Counts one arrival of `n` under `token`; true for the last, which clears the word.
 QG_DEV_INLINE bool fp8_arrive(unsigned long long* word, unsigned long long token, int n)
 {
-    unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
+    unsigned long long old = 0;   // what it holds between launches, mostly
     for (;;) {
         const unsigned long long have = (old & ~0xFFull) == token ? old & 0xFFull : 0ull;
         const bool last = have + 1 == (unsigned long long)n;
         const unsigned long long seen = atomicCAS(word, old, last ? 0ull : token | (have + 1));
         if (seen == old) return last;
         old = seen;
-    }
-}
-
-template <int NT>
-__global__ void __launch_bounds__(Fp8StreamCfg<NT>::THREADS, 1)
-    fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w,
-                      const __grid_constant__ CUtensorMap tm_x)
-{
-    using C = Fp8StreamCfg<NT>;
-    constexpr int ST = C::ST, DB = C::DB, SC = C::SC;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* scales = reinterpret_cast<float*>(smem + C::SC_OFF);   // [SC][2][NT]
-    Fp8Sched& sched = *reinterpret_cast<Fp8Sched*>(smem + C::SCHED_OFF);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
-    uint64_t* empty = full + ST;
-    uint64_t* dfull = empty + ST;
-    uint64_t* dempty = dfull + DB;
-    uint64_t* sfull = dempty + DB;
-    uint64_t* sempty = sfull + SC;
-    uint64_t* done = sempty + SC;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 2);
-    __shared__ int s_last;
-
-    const int warp = uniform_warp(), lane = threadIdx.x & 31;
-    const int G = p.G, slabs = (p.N + 255) / 256;
-
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < ST; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
-        }
-        for (int i = 0; i < DB; ++i) {
-            mbar_init(&dfull[i], 1);
-            mbar_init(&dempty[i], C::EPI);
-        }
-        for (int i = 0; i < SC; ++i) {
-            mbar_init(&sfull[i], 1);
-            mbar_init(&sempty[i], C::EPI);
-        }
-        mbar_init(&done[0], 1);
-        mbar_init(&done[1], 1);
-        fence_mbar_init();
-        tma_prefetch_desc(&tm_w);
-        tma_prefetch_desc(&tm_x);
-    }
-    // the experts' offsets come from the kernel before; a dense product's schedule does not
-    if (p.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!fp8_schedule<NT>(sched, p, slabs)) return;
-    const int64_t units = (int64_t)sched.pre[p.E] * G;
-    const int grid = (int)min((int64_t)gridDim.x, units);
-    if ((int)blockIdx.x >= grid) return;
-    const int64_t u0 = fp8_first_unit(blockIdx.x, units, grid);
-    const int n_it = (int)(fp8_first_unit(blockIdx.x + 1, units, grid) - u0);
-    const int tile0 = (int)(u0 / G), kb0 = (int)(u0 - (int64_t)tile0 * G);
-    if (warp == 1) {
-        tmem_alloc(tslot, C::TMEM_COLS);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tslot;
-
-    Fp8Walk<NT> walk(sched, p.E, slabs);
-    walk.at(tile0);
-    if (warp < 4) {
-        if constexpr (NT == 128) setmaxnreg_dec<72>();
-        if (warp == 0) {
-            // ---------------- producer ----------------
-            int kb = kb0, i = 0, y[4];
-            const bool one = elect_one();
-            const int early = p.offsets ? 0 : min(ST, n_it);
-            auto weights = [&](int s, const Fp8Walk<NT>& w, int k) {
-                uint8_t* st = smem + s * C::STAGE;
-                mbar_arrive_expect_tx(&full[s], C::STAGE);
-                tma_load_3d(&tm_w, &full[s], st, w.slab * 256, k * 128, w.e);
-                tma_load_3d(&tm_w, &full[s], st + 16384, w.slab * 256 + 128, k * 128, w.e);
-            };
-            if (early) {
-                // weights do not depend on the kernel before: the ring's first are requested
-                // before waiting for it
-                Fp8Walk<NT> w = walk;
-                for (int j = 0, k = kb0; j < early; ++j) {
-                    if (one) weights(j, w, k);
-                    if (++k == G) { k = 0; w.next(); }
-                }
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-            }
-            if (p.rows) fp8_gather_rows(p, walk.first(), walk.rows(), lane, y);
-            bool ok = true;
-            for (; i < n_it; ++i) {
-                const int s = i % ST;
-                if (i >= early) {
-                    ok = all_wait(&empty[s], ((i / ST) & 1) ^ 1);
-                    if (!ok) break;
-                    if (one) weights(s, walk, kb);
-                    __syncwarp();
-                }
-                uint8_t* xt = smem + s * C::STAGE + C::W_BYTES;
-                if (!p.rows) {
-                    if (one) tma_load_2d(&tm_x, &full[s], xt, kb * 128, walk.first());
-                } else if (lane < NT / 4) {
-                    tma_gather4(&tm_x, &full[s], xt + lane * 512, kb * 128, y);
-                }
-                if (++kb == G) {
-                    kb = 0;
-                    walk.next();
-                    if (p.rows && i + 1 < n_it) fp8_gather_rows(p, walk.first(), walk.rows(), lane, y);
-                }
-            }
-            if (!ok)   // copies in flight land before the block leaves
-                for (int j = max(i - ST, 0); j < i; ++j) all_wait(&full[j % ST], (j / ST) & 1);
-        } else if (warp & 1) {
-            // ------- MMA issuers: warp 1 the even units, warp 3 the odd ones, so that one's waits
-            // lie beside the other's MMAs -------
-            constexpr uint32_t idesc = idesc_e4m3(NT, true, false);
-            const uint64_t w0 = smem_desc(smem_u32(smem), 16384, 1024, 2), x0 = smem_desc(smem_u32(smem + C::W_BYTES), 16, 1024, 2);
-            const bool one = elect_one();
-            const int e = warp >> 1;
-            int i = e, s = e, b = e;
-            uint32_t sp = 0, bp = 1;   // parities
-            for (; i < n_it; i += 2) {
-                if (!all_wait(&full[s], sp) || !all_wait(&dempty[b], bp)) break;
-                tc_fence_after();
-                if (one) {
-                    const uint64_t w = w0 + s * (C::STAGE >> 4), x = x0 + s * (C::STAGE >> 4);
-                    const uint32_t d = tmem + 2 * b * NT;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_e4m3_ss(d + h * NT, w + h * (16384 >> 4) + kk * (4096 >> 4), x + kk * (32 >> 4), idesc, kk > 0 ? 1u : 0u);
-                    mma_commit(&dfull[b]);
-                    mma_commit(&empty[s]);
-                }
-                __syncwarp();
-                if ((s += 2) >= ST) { s = e; sp ^= 1; }
-                if ((b += 2) >= DB) { b = e; bp ^= 1; }
-            }
-            if (i > 1) {   // every MMA has completed before tensor memory is released
-                if (one) mma_commit(&done[e]);
-                __syncwarp();
-                all_wait(&done[e], 0);
-            }
-        } else if (warp == 2) {
-            // ---------------- scales ----------------
-            if (!p.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
-            constexpr int R = (NT + 31) / 32;
-            Fp8Scales<NT, R> sc(p, walk, n_it, kb0, lane);
-            bool ok = true;
-            int i = 0;
-            while (ok && sc.advance()) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j < sc.n && ok) {
-                        const int b = i % SC;
-                        ok = all_wait(&sempty[b], ((i / SC) & 1) ^ 1);
-                        if (ok) {
-                            float* o = scales + b * 2 * NT;
-#pragma unroll
-                            for (int r = 0; r < R; ++r)
-                                if (lane + 32 * r < NT) {
-                                    o[lane + 32 * r] = __fmul_rn(sc.x[r][j], sc.w[0][j]);
-                                    o[NT + lane + 32 * r] = __fmul_rn(sc.x[r][j], sc.w[1][j]);
-                                }
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sfull[b]);
-                            ++i;
-                        }
-                    }
-                }
-            }
-        }
-    } else {
-        if constexpr (NT == 128) setmaxnreg_inc<216>();
-        // ---------------- fold: thread = column ----------------
-        asm volatile("griddepcontrol.wait;" ::: "memory");   // Y and the workspace follow the kernel before
-        const int q = warp & 3, half = (warp - 4) >> 2, col = half * 128 + 32 * q + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + half * NT;
-        float acc[NT];
-        bool ok = true;
-        int i = 0, kb = kb0;
-        while (i < n_it) {
-            const int ie = min(n_it, i + G - kb);   // this piece: units [i, ie)
-            const bool head = kb == 0, whole = head && ie - i == G;
-            const int64_t first = u0 + i - kb;      // the tile's first unit
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[t] = 0.0f;
-            for (; i < ie; ++i) {
-                const int b = i % DB, sl = i % SC;
-                if (ok) ok = all_wait(&sfull[sl], (i / SC) & 1) && all_wait(&dfull[b], (i / DB) & 1);
-                if (!ok) continue;
-                tc_fence_after();
-                fp8_fold<NT, true>(acc, lanes + b * 2 * NT, scales + (2 * sl + half) * NT, 0.0f, [&]() {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&dempty[b]);
-                        mbar_arrive(&sempty[sl]);
-                    }
-                });
-            }
-            const int rows = walk.rows(), s0 = walk.first(), n = walk.slab * 256 + col;
-            bool write = whole;
-            if (!whole) {
-                float* mine = p.partials + ((int64_t)blockIdx.x * 2 + (head ? 1 : 0)) * C::PARTIAL + col;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    if ((t & ~15) < rows) __stcg(mine + t * 256, acc[t]);
-                // the pieces of this tile are CTAs cf .. cl
-                const int cf = head ? (int)blockIdx.x : fp8_cta_of_unit(first, units, grid);
-                const int cl = fp8_cta_of_unit(first + G - 1, units, grid);
-                __threadfence();
-                named_bar_sync(1, 32 * C::EPI);
-                if (threadIdx.x == 128) {
-                    s_last = fp8_arrive(p.counters + cf, p.token, cl - cf + 1);
-                    __threadfence();
-                }
-                named_bar_sync(1, 32 * C::EPI);
-                write = s_last;
-                if (write) {
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) acc[t] = 0.0f;
-                    for (int c = cf; c <= cl; ++c) {
-                        const float* o = p.partials + ((int64_t)c * 2 + (c == cf ? 1 : 0)) * C::PARTIAL + col;
-#pragma unroll
-                        for (int t0 = 0; t0 < NT; t0 += 16) {   // 16 loads in flight
-                            if (t0 < rows) {
-                                float v[16];
-#pragma unroll
-                                for (int t = 0; t < 16; ++t) v[t] = __ldcg(o + (t0 + t) * 256);
-#pragma unroll
-                                for (int t = 0; t < 16; ++t) acc[t0 + t] += v[t];
-                            }
-                        }
-                    }
-                }
-                named_bar_sync(1, 32 * C::EPI);   // s_last has been read
-            }
-            if (write && ok) {
-                uint32_t zero[(NT + 31) / 32];   // rows whose map entry is wrong
-#pragma unroll
-                for (int r = 0; r < (NT + 31) / 32; ++r) {
-                    const int t = lane + 32 * r;
-                    zero[r] = p.rows ? __ballot_sync(0xffffffffu, t < rows && fp8_row(p, s0 + t) < 0) : 0u;
-                }
-                auto store = [&](auto bf) {
-                    // lane pairs exchange, so that a lane stores two adjacent columns of a row
-                    const int odd = lane & 1;
-                    uint16_t* y = p.Y + (int64_t)(s0 + odd) * p.N + n - odd;
-#pragma unroll
-                    for (int t = 0; t < NT; t += 2) {
-                        if ((t & ~15) >= rows) break;
-                        uint32_t ab = fp8_out2<decltype(bf)::value>(acc[t], acc[t + 1]);   // two rows of a column
-                        if (zero[t / 32] >> (t & 31) & 1u) ab &= 0xFFFF0000u;
-                        if (zero[t / 32] >> ((t + 1) & 31) & 1u) ab &= 0xFFFFu;
-                        const uint32_t got = __shfl_xor_sync(0xffffffffu, ab, 1);
-                        if (t + odd < rows && n < p.N)
-                            *reinterpret_cast<uint32_t*>(y + (int64_t)t * p.N) = odd ? prmt(got, ab, 0x7632) : prmt(ab, got, 0x5410);
-                    }
-                };
-                if (p.bf16) store(std::true_type{});
-                else store(std::false_type{});
-            }
-            kb = 0;
-            walk.next();
-        }
-    }
-
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, C::TMEM_COLS);
     }
 }
 
@@ -676,28 +310,74 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const Fp8Params p, const 
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: 128 rows x BN columns, one group of K a step, persistent.
+// The product: tiles of 128 rows x BN columns, one group of K a step, persistent.
 //
-// Mapped rows are gathered by fp8_rows_kernel before it (TMA's gather of four rows an
-// instruction took three times as long as a step's MMAs).
+// Roles: warp 0 TMA; warps 1 and 3 issue the MMAs of even and odd steps, into DB buffers; warps
+// 4..11 fold: thread = row, BN / 2 columns, whose weight scale is one number, so a step costs a
+// thread one scale (which it loads itself, four groups ahead) and BN / 2 fma.
 //
-// Roles: warp 0 TMA; warps 1 and 3 issue the MMAs, step by step into DB buffers; warps 4..11
-// fold: thread = row, BN / 2 columns, whose weight scale is one number, so a step costs a thread
-// one scale and BN / 2 fma.
+// Few rows: the tensor core then multiplies mostly zeros, but a step's weights (16 or 32 KB)
+// take HBM as long as a step takes the tensor core.  Mapped rows are gathered by
+// fp8_rows_kernel before it (TMA's gather of four rows an instruction took three times as long
+// as a step's MMAs).
 // ---------------------------------------------------------------------------
 template <int BN>
 struct Fp8TileCfg {
     static constexpr int BM = 128, DB = 512 / BN;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
-    static constexpr int ST = BN == 256 ? 4 : 6;
-    static constexpr int THREADS = 384;
+    static constexpr int ST = BN == 256 ? 4 : 6;          // even: a stage always serves the same issuer
+    static constexpr int THREADS = 384, TMEM_COLS = DB * BN;
     static constexpr int OUT_OFF = ST * STAGE;            // per fold warp: 32 rows x 32 columns of Y
     static constexpr int SCHED_OFF = OUT_OFF + 8 * 32 * 64;
     static constexpr int BAR_OFF = SCHED_OFF + (int)((sizeof(Fp8Sched) + 15) / 16 * 16);
     static constexpr int NBAR = 2 * ST + 2 * DB + 2;
     static constexpr int TOTAL = BAR_OFF + NBAR * 8 + 16 + 1024;
-    static_assert(TOTAL <= 227 * 1024 && ST % 2 == 0, "tile kernel shared memory");
+    static constexpr int PARTIAL = 128 * BN;              // floats of a piece's sums
+    static_assert(TOTAL <= 227 * 1024 - 64 && ST % 2 == 0, "tile kernel shared memory");
 };
+
+// The 256 folding threads: the sums of pieces cf .. cl of a tile, added in that order, to Y.  PER
+// times four columns and PIECES pieces a thread are in flight.
+template <int BN, int PER, int PIECES>
+QG_DEV_INLINE void fp8_join(const Fp8Params& p, int s0, int rows, int n0, int cf, int cl)
+{
+    const int count = min(rows, 128) * (BN / 4);
+    const float4* base = reinterpret_cast<const float4*>(p.partials);
+    for (int e0 = threadIdx.x - 128; e0 < count; e0 += 256 * PER) {
+        float4 a[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) a[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int c0 = cf; c0 <= cl; c0 += PIECES) {
+            float4 v[PIECES][PER];
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const int c = c0 + i;
+                const float4* o = base + ((int64_t)c * 2 + (c == cf ? 1 : 0)) * (Fp8TileCfg<BN>::PARTIAL / 4) + e0;
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    v[i][j] = c <= cl && e0 + 256 * j < count ? __ldcg(o + 256 * j) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    a[j].x += v[i][j].x;
+                    a[j].y += v[i][j].y;
+                    a[j].z += v[i][j].z;
+                    a[j].w += v[i][j].w;
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int e = e0 + 256 * j, r = e / (BN / 4), n = n0 + 4 * (e % (BN / 4));
+            if (e >= count || n >= p.N) continue;
+            uint2 v = p.bf16 ? make_uint2(pack_bf16x2_rn(a[j].x, a[j].y), pack_bf16x2_rn(a[j].z, a[j].w))
+                             : make_uint2(pack_f16x2_rn(a[j].x, a[j].y), pack_f16x2_rn(a[j].z, a[j].w));
+            if (fp8_row(p, s0 + r) < 0) v = make_uint2(0u, 0u);   // a wrong map entry
+            *reinterpret_cast<uint2*>(p.Y + (int64_t)(s0 + r) * p.N + n) = v;
+        }
+    }
+}
 
 template <int BN>
 __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
@@ -714,9 +394,12 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
     uint64_t* dempty = dfull + DB;
     uint64_t* done = dempty + DB;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(done + 2);
+    __shared__ int s_last;
+    __shared__ Fp8Work work;
 
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int G = p.G, slabs = (p.N + BN - 1) / BN;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
@@ -732,42 +415,59 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
         tma_prefetch_desc(&tm_w);
         tma_prefetch_desc(&tm_x);
     }
+    // the experts' offsets come from the kernel before; a dense product's schedule does not
     if (p.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!fp8_schedule<C::BM>(sched, p, slabs)) return;
-    const int tiles = sched.pre[p.E];
-    if ((int)blockIdx.x >= tiles) return;
+    if (threadIdx.x == 0) work.init(sched.pre[p.E], p.box, G, gridDim.x, blockIdx.x);
+    __syncthreads();
+    if (work.steps() == 0) return;
     if (warp == 1) {
-        tmem_alloc(tslot, C::DB * BN);
+        tmem_alloc(tslot, C::TMEM_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    Fp8Walk<C::BM> walk(sched, p.E, slabs);
 
     if (warp < 4) {
         setmaxnreg_dec<72>();
         if (warp == 0) {
             // ---------------- producer ----------------
+            Fp8Walk<C::BM> walk(sched, p.E, slabs);
             const bool one = elect_one();
+            auto weights = [&](int s, int n0, int kb) {
+                uint8_t* st = smem + s * C::STAGE;
+                mbar_arrive_expect_tx(&full[s], C::B_BYTES + p.box * 128);
+                tma_load_3d(&tm_w, &full[s], st + C::A_BYTES, n0, kb * 128, walk.e);
+                if (BN == 256) tma_load_3d(&tm_w, &full[s], st + C::A_BYTES + 16384, n0 + 128, kb * 128, walk.e);
+            };
+            // weights do not depend on the kernel before: a dense product's first stages of them
+            // are requested before waiting for it
+            int early = 0, tile, k0, k1;
+            if (!p.offsets) {
+                for (int i = 0; early < ST && work.piece(i, tile, k0, k1); ++i) {
+                    walk.at(tile);
+                    for (int kb = k0; kb < k1 && early < ST; ++kb, ++early)
+                        if (one) weights(early, walk.slab * BN, kb);
+                }
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+            }
             bool ok = true;
             int64_t issued = 0;
-            asm volatile("griddepcontrol.wait;" ::: "memory");
             int s = 0;
             uint32_t sp = 1;   // parity
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            for (int i = 0; ok && work.piece(i, tile, k0, k1); ++i) {
                 walk.at(tile);
                 const int s0 = walk.first(), n0 = walk.slab * BN;
-                for (int kb = 0; kb < G; ++kb) {
-                    ok = all_wait(&empty[s], sp);
-                    if (!ok) break;
-                    uint8_t* st = smem + s * C::STAGE;
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (issued >= early) {
+                        ok = all_wait(&empty[s], sp);
+                        if (!ok) break;
+                    }
                     if (one) {
-                        mbar_arrive_expect_tx(&full[s], C::STAGE);
-                        tma_load_3d(&tm_w, &full[s], st + C::A_BYTES, n0, kb * 128, walk.e);
-                        if (BN == 256) tma_load_3d(&tm_w, &full[s], st + C::A_BYTES + 16384, n0 + 128, kb * 128, walk.e);
-                        tma_load_2d(&tm_x, &full[s], st, kb * 128, s0);
+                        if (issued >= early) weights(s, n0, kb);
+                        tma_load_2d(&tm_x, &full[s], smem + s * C::STAGE, kb * 128, s0);
                     }
                     __syncwarp();
                     if (++s == ST) { s = 0; sp ^= 1; }
@@ -777,13 +477,12 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
             if (!ok)   // copies in flight land before the block leaves
                 for (int64_t j = issued > ST ? issued - ST : 0; j < issued; ++j) all_wait(&full[j % ST], (int)(j / ST) & 1);
         } else if (warp & 1) {
-            // ------- MMA issuers: warp 1 the even units, warp 3 the odd ones, so that one's waits
-            // lie beside the other's MMAs -------
+            // ---------------- MMA issuers (two, so that one's waits lie beside the other's MMAs) ----------------
             constexpr uint32_t idesc = idesc_e4m3(BN, false, true);
             const uint64_t a0 = smem_desc(smem_u32(smem), 16, 1024, 2);
             const uint64_t b0 = smem_desc(smem_u32(smem + C::A_BYTES), 16384, 1024, 2);
             const bool one = elect_one();
-            const int64_t steps = (int64_t)((tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * G;
+            const int64_t steps = work.steps();
             const int e = warp >> 1;
             int64_t i = e;
             int s = e, b = e;
@@ -818,18 +517,8 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
         const bool vec = G % 4 == 0;   // then every row of xs starts on 16 bytes
         // the scales of this thread's row and columns, four groups at a time, the next four loading
         float x[4], w[4];
-        int s0, rows, n0, row;
+        int s0, rows, n0, row, tile, k0, k1;
         const float *xp, *wp;
-        auto open = [&](int tile) {
-            walk.at(tile);
-            s0 = walk.first() + 32 * q;
-            rows = walk.rows() - 32 * q;
-            n0 = walk.slab * BN + half * HW;
-            row = lane < rows ? fp8_row(p, s0 + lane) : -2;
-            if (row == -1 && walk.slab == 0 && half == 0) set_status(6u);
-            xp = p.xs + (int64_t)max(row, 0) * G;
-            wp = p.ws + (int64_t)walk.e * G * p.NB + min(n0 / 128, p.NB - 1);
-        };
         auto load = [&](int kb) {
             if (vec) {
                 const float4 v = __ldg(reinterpret_cast<const float4*>(xp + kb));
@@ -841,28 +530,40 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = __ldg(wp + (int64_t)min(kb + j, G - 1) * p.NB);
         };
-        bool ok = true;
+        auto open = [&]() {
+            Fp8Walk<C::BM> walk(sched, p.E, slabs);
+            walk.at(tile);
+            s0 = walk.first() + 32 * q;
+            rows = walk.rows() - 32 * q;
+            n0 = walk.slab * BN + half * HW;
+            row = lane < rows ? fp8_row(p, s0 + lane) : -2;
+            if (row == -1 && walk.slab == 0 && half == 0) set_status(6u);
+            xp = p.xs + (int64_t)max(row, 0) * G;
+            wp = p.ws + (int64_t)walk.e * G * p.NB + min(n0 / 128, p.NB - 1);
+            load(k0 & ~3);
+        };
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // xs, Y and the workspace follow the kernel before
+        bool ok = true, more = work.piece(0, tile, k0, k1);
         int b = 0;
         uint32_t bp = 0;
-        asm volatile("griddepcontrol.wait;" ::: "memory");   // xs and Y follow the kernel before
-        open(blockIdx.x);
-        load(0);
-        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        open();
+        for (int i = 0; more && ok; ++i) {
             float acc[HW];
 #pragma unroll
             for (int t = 0; t < HW; ++t) acc[t] = 0.0f;
-            for (int k0 = 0; k0 < G && ok; k0 += 4) {
+            for (int k4 = k0 & ~3; k4 < k1 && ok; k4 += 4) {
                 float sc[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) sc[j] = row >= 0 ? __fmul_rn(x[j], w[j]) : 0.0f;
-                if (k0 + 4 < G) load(k0 + 4);
+                if (k4 + 4 < k1) load(k4 + 4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (k0 + j >= G || !ok) break;
+                    if (k4 + j < k0) continue;
+                    if (k4 + j >= k1 || !ok) break;
                     ok = all_wait(&dfull[b], bp);
                     if (!ok) break;
                     tc_fence_after();
-                    fp8_fold<HW, false>(acc, lanes + b * BN, nullptr, sc[j], [&]() {
+                    fp8_fold<HW>(acc, lanes + b * BN, sc[j], [&]() {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&dempty[b]);
@@ -870,14 +571,36 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
                     if (++b == DB) { b = 0; bp ^= 1; }
                 }
             }
-            if (!ok) break;
-            // Y: 32 x 32 blocks turned in shared memory, so that four lanes store 64 bytes of a row
             const bool zero = row < 0;
-            const int os0 = s0, orows = rows, on0 = n0;
-            if (tile + (int)gridDim.x < tiles) {
-                open(tile + gridDim.x);
-                load(0);
+            const int os0 = s0, orows = rows, on0 = n0, ok0 = k0, ok1 = k1;
+            more = work.piece(i + 1, tile, k0, k1);
+            if (more) open();   // its scales load meanwhile
+            bool write = ok;
+            if (ok0 > 0 || ok1 < G) {   // a piece of a split tile
+                const int64_t first = work.u0 + (i > work.whole ? work.n - ok1 : -ok0);   // the tile's first unit
+                const int cf = work.cta_of(first), cl = work.cta_of(first + G - 1);
+                float4* mine = reinterpret_cast<float4*>(p.partials + ((int64_t)blockIdx.x * 2 + (ok0 == 0 ? 1 : 0)) * C::PARTIAL +
+                                                         (32 * q + lane) * BN + half * HW);
+                if (lane < orows)
+#pragma unroll
+                    for (int c = 0; c < HW / 4; ++c)
+                        __stcg(mine + c, make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]));
+                named_bar_sync(1, 256);
+                if (threadIdx.x == 128) {
+                    __threadfence();   // of all 256 threads' stores, by the barrier
+                    s_last = fp8_arrive(p.counters + cf, p.token, cl - cf + 1);
+                    __threadfence();
+                }
+                named_bar_sync(1, 256);
+                write = false;
+                if (ok && s_last) {
+                    const int tr = orows + 32 * q;   // the tile's rows
+                    if (tr * (BN / 4) <= 256) fp8_join<BN, 1, 8>(p, os0 - 32 * q, tr, on0 - half * HW, cf, cl);
+                    else fp8_join<BN, 4, 4>(p, os0 - 32 * q, tr, on0 - half * HW, cf, cl);
+                }
+                named_bar_sync(1, 256);   // s_last has been read
             }
+            // Y: 32 x 32 blocks turned in shared memory, so that four lanes store 64 bytes of a row
             auto store = [&](auto bf) {
 #pragma unroll
                 for (int c = 0; c < HW; c += 32) {
@@ -900,6 +623,7 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
                     }
                 }
             };
+            if (!write) continue;
             if (p.bf16) store(std::true_type{});
             else store(std::false_type{});
         }
@@ -909,7 +633,7 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::DB * BN);
+        tmem_dealloc(tmem, C::TMEM_COLS);
     }
 }
 

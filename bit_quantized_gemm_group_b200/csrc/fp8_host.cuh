@@ -33,63 +33,37 @@ qg_status quantize_weight_fp8(const void* W, int E, int K, int N, uint8_t* Wq, f
 // ---------------------------------------------------------------------------
 bool fp8_bad_shape(int K, int N) { return K < 16 || K % 16 || N < 16 || N % 16; }
 
-// Rows per tile of the stream kernel for so many rows (an expert's on average), 0: the tile
-// kernel.
-int fp8_stream_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 256 ? 128 : 0; }
-
+// The workspace: counters and partial sums of split tiles, then (mapped rows) the rows in slot
+// order.  256 columns a tile are assumed: the number of experts, and so the choice, is not known.
 struct Fp8Workspace {
-    size_t first, bytes;   // the first part's, and all
+    size_t partials, rows, bytes;   // where the second and third part start, and all
 };
 
-Fp8Workspace fp8_stream_workspace(int nt)
+Fp8Workspace fp8_carve(int S, int K, bool experts)
 {
-    const size_t grid = num_sms(), c = (grid * 8 + 255) / 256 * 256;
-    return {c, c + grid * 2 * nt * 256 * sizeof(float)};
+    const size_t grid = num_sms();
+    Fp8Workspace w;
+    w.partials = (grid * 8 + 255) / 256 * 256;
+    w.rows = w.partials + grid * 2 * 128 * 256 * sizeof(float);
+    w.bytes = w.rows + (experts ? (size_t)S * K : 0);
+    return w;
 }
 
-// A size that serves every number of experts, for the experts' product: the stream kernel's,
-// and the tile kernel's rows in slot order.
-size_t fp8_workspace(int S, int K, bool experts)
-{
-    const int nt = experts && S > 64 ? 128 : fp8_stream_rows(S);
-    const size_t stream = nt ? fp8_stream_workspace(nt).bytes : 0;
-    return experts && !fp8_stream_rows(S) ? std::max(stream, (size_t)S * K) : stream;
-}
+size_t fp8_workspace(int S, int K, bool experts) { return fp8_carve(S, K, experts).bytes; }
 
-// The weights as {N, K, E} (boxes of 128 columns x 128 k), the activations as {K, Mx}
-// (boxes of 128 k x `box` rows, or of one row to be gathered).
-qg_status fp8_maps(CUtensorMap* tw, CUtensorMap* tx, const uint8_t* Xq, const uint8_t* Wq, const qg::Fp8Params& p, int box)
+// The weights as {N, K, E} (boxes of 128 columns x 128 k), the activations as {K, rows} (boxes of
+// 128 k x p.box rows).
+qg_status fp8_maps(CUtensorMap* tw, CUtensorMap* tx, const uint8_t* X, int rows, const uint8_t* Wq, const qg::Fp8Params& p)
 {
     const uint64_t N = p.N, K = p.K;
     qg_status st = make_tmap_3d(tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, Wq, N, K, p.E, N, N * K, 128, 128, 1,
                                 CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != QG_OK) return st;
-    return make_tmap_2d(tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, Xq, K, p.Mx, 128, p.rows ? 1 : box,
-                        CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-template <int NT>
-qg_status launch_fp8_stream(qg::Fp8Params p, const uint8_t* Xq, const uint8_t* Wq, void* ws, qg_stream_t stream)
-{
-    using C = qg::Fp8StreamCfg<NT>;
-    auto kern = qg::fp8_stream_kernel<NT>;
-    static KernelInfo info;
-    int occ = 1;
-    qg_status st = prepare_kernel(info, kern, C::THREADS, C::TOTAL, &occ);
-    if (st != QG_OK) return st;
-    CUtensorMap tw, tx;
-    if ((st = fp8_maps(&tw, &tx, Xq, Wq, p, NT)) != QG_OK) return st;
-    p.counters = static_cast<unsigned long long*>(ws);
-    p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + fp8_stream_workspace(NT).first);
-    do p.token = next_decode_token() << 8;
-    while (p.token == 0);
-    int grid = num_sms();
-    if (!p.offsets) grid = (int)std::min<int64_t>(grid, (int64_t)((p.S + NT - 1) / NT) * ((p.N + 255) / 256) * p.G);
-    return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::TOTAL, stream, p, tw, tx);
+    return make_tmap_2d(tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, X, K, rows, 128, p.box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int BN>
-qg_status launch_fp8_tile(qg::Fp8Params p, const uint8_t* Xq, const uint8_t* Wq, void* ws, qg_stream_t stream)
+qg_status launch_fp8_tile(qg::Fp8Params p, const uint8_t* X, const uint8_t* Wq, void* ws, qg_stream_t stream)
 {
     using C = qg::Fp8TileCfg<BN>;
     auto kern = qg::fp8_tile_kernel<BN>;
@@ -97,33 +71,33 @@ qg_status launch_fp8_tile(qg::Fp8Params p, const uint8_t* Xq, const uint8_t* Wq,
     int occ = 1;
     qg_status st = prepare_kernel(info, kern, C::THREADS, C::TOTAL, &occ);
     if (st != QG_OK) return st;
-    CUtensorMap tw, tx;
-    qg::Fp8Params x = p;   // the rows as the kernel reads them
+    const Fp8Workspace w = fp8_carve(p.S, p.K, p.rows != nullptr);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    p.counters = reinterpret_cast<unsigned long long*>(base);
+    p.partials = reinterpret_cast<float*>(base + w.partials);
+    do p.token = next_decode_token() << 8;
+    while (p.token == 0);
+    int rows = p.Mx;
     if (p.rows) {
         const dim3 g((p.S + 3) / 4, (p.K + 4095) / 4096);
-        if ((st = launch_pdl(qg::fp8_rows_kernel, g, dim3(256), 0, stream, p, Xq, static_cast<uint8_t*>(ws))) != QG_OK) return st;
-        Xq = static_cast<const uint8_t*>(ws);
-        x.rows = nullptr;
-        x.Mx = p.S;
+        if ((st = launch_pdl(qg::fp8_rows_kernel, g, dim3(256), 0, stream, p, X, base + w.rows)) != QG_OK) return st;
+        X = base + w.rows;
+        rows = p.S;
     }
-    if ((st = fp8_maps(&tw, &tx, Xq, Wq, x, 128)) != QG_OK) return st;
-    // at most so many tiles: every expert may end inside one
-    const int64_t rows = (int64_t)(p.S + C::BM - 1) / C::BM + (p.offsets ? std::min(p.S, p.E) : 0);
-    const int grid = (int)std::min<int64_t>(num_sms(), rows * ((p.N + BN - 1) / BN));
-    return launch_pdl(kern, dim3(grid), dim3(C::THREADS), C::TOTAL, stream, p, tw, tx);
+    CUtensorMap tw, tx;
+    if ((st = fp8_maps(&tw, &tx, X, rows, Wq, p)) != QG_OK) return st;
+    return launch_pdl(kern, dim3(num_sms()), dim3(C::THREADS), C::TOTAL, stream, p, tw, tx);
 }
 
 qg_status fp8_gemm(const uint8_t* Xq, const float* xs, int Mx, int K, const int32_t* rows, const int32_t* offsets, int S,
                    int E, const uint8_t* Wq, const float* ws, int N, void* Y, qg_dtype ydt, void* workspace,
                    size_t ws_bytes, qg_stream_t stream)
 {
-    if (!Xq || !xs || !Wq || !ws || !Y) return QG_ERR_NULL;
+    if (!Xq || !xs || !Wq || !ws || !Y || !workspace) return QG_ERR_NULL;
     if (misaligned(Xq) || misaligned(xs) || misaligned(rows) || misaligned(offsets) || misaligned(Wq) ||
         misaligned(ws) || misaligned(Y) || misaligned(workspace))
         return QG_ERR_ALIGN;
-    const size_t need = fp8_workspace(S, K, offsets != nullptr);
-    if (need && !workspace) return QG_ERR_NULL;
-    if (need > ws_bytes) return QG_ERR_WORKSPACE;
+    if (ws_bytes < fp8_workspace(S, K, offsets != nullptr)) return QG_ERR_WORKSPACE;
     qg::Fp8Params p{};
     p.xs = xs;
     p.ws = ws;
@@ -138,16 +112,10 @@ qg_status fp8_gemm(const uint8_t* Xq, const float* xs, int Mx, int K, const int3
     p.G = (K + 127) / 128;
     p.NB = (N + 127) / 128;
     p.bf16 = ydt == QG_BF16;
-    switch (fp8_stream_rows(offsets ? ((int64_t)S + E - 1) / E : S)) {
-        case 16: return launch_fp8_stream<16>(p, Xq, Wq, workspace, stream);
-        case 32: return launch_fp8_stream<32>(p, Xq, Wq, workspace, stream);
-        case 64: return launch_fp8_stream<64>(p, Xq, Wq, workspace, stream);
-        case 128: return launch_fp8_stream<128>(p, Xq, Wq, workspace, stream);
-        default: break;
-    }
-    // 256 columns a tile where the tiles then still fill the GPU
+    p.box = S >= 128 ? 128 : (S + 7) / 8 * 8;   // the rest of a tile holds what it held: rows of sums that go nowhere
+    // 256 columns a tile where those tiles still fill half of the GPU
     const int64_t m_tiles = (int64_t)(S + 127) / 128 + (offsets ? std::min(S, E) / 2 : 0);
-    if (m_tiles * ((N + 255) / 256) < num_sms()) return launch_fp8_tile<128>(p, Xq, Wq, workspace, stream);
+    if (m_tiles * ((N + 255) / 256) * 2 < num_sms()) return launch_fp8_tile<128>(p, Xq, Wq, workspace, stream);
     return launch_fp8_tile<256>(p, Xq, Wq, workspace, stream);
 }
 
