@@ -336,12 +336,13 @@ _SCORES = {"softmax": QG_SCORE_SOFTMAX, "sigmoid": QG_SCORE_SIGMOID}
 
 
 def _want(where, name, t, types, shape, device):
+    """t has one of the types, the shape, lies on GPU `device` (an index) and is contiguous."""
     if t.dtype not in types:
         raise ValueError(f"{where}: {name} has dtype {t.dtype}, not one of {', '.join(map(str, types))}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, not {shape}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{where}: {name} is on {t.device}: all tensors have to be on one GPU ({device})")
+    if t.shape != shape:
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if device < 0 or t.get_device() != device:
+        raise ValueError(f"{where}: {name} is on {t.device}: all tensors have to be on one GPU")
     if not t.is_contiguous():
         raise ValueError(f"{where}: {name} has to be contiguous (row-major)")
 
@@ -351,26 +352,26 @@ def _rank(where, name, t, n):
         raise ValueError(f"{where}: {name} has {t.dim()} dimensions, not {n}")
 
 
-def _cdiv(a, b):
-    return -(-a // b)
-
-
 def _run(where, device, stream, args, op=None, workspace=None):
-    """Calls `where` with `args`, then (op = (op, M, K, N)) the workspace, then the stream, on `device`."""
-    with torch.cuda.device(device):
-        st = torch.cuda.current_stream(device) if stream is None else stream
-        if op is not None:
-            need = lib().qg_workspace_size(*op)
-            if isinstance(workspace, str) and workspace == "auto":
-                workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-                if workspace is not None and stream is not None:
-                    workspace.record_stream(stream)
-            if workspace is None or workspace is False:
-                args += (None, 0)
-            else:
-                _want(where, "workspace", workspace, (torch.uint8,), (workspace.numel(),), device)
-                args += (workspace.data_ptr(), workspace.numel())
-        _check(getattr(lib(), where)(*args, st.cuda_stream), where)
+    """Calls `where` with `args`, then (op = (op, M, K, N)) the workspace, then the stream, on GPU `device`."""
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _run(where, device, stream, args, op, workspace)
+    f = getattr(lib(), where)
+    if op is not None:
+        if isinstance(workspace, str) and workspace == "auto":
+            need = _lib.qg_workspace_size(*op)
+            workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+            if workspace is not None and stream is not None:
+                workspace.record_stream(stream)
+        if workspace is None or workspace is False:
+            args += (None, 0)
+        else:
+            _want(where, "workspace", workspace, (torch.uint8,), (workspace.numel(),), device)
+            args += (workspace.data_ptr(), workspace.numel())
+    st = f(*args, torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream)
+    if st != QG_OK:
+        raise QgError(st, where)
 
 
 def qg_quantize_act_fp8(X, Xq, xs, stream=None):
@@ -378,10 +379,10 @@ def qg_quantize_act_fp8(X, Xq, xs, stream=None):
     f = "qg_quantize_act_fp8"
     _rank(f, "X", X, 2)
     M, K = X.shape
-    _want(f, "X", X, _HALF, (M, K), X.device)
-    _want(f, "Xq", Xq, _E4M3, (M, K), X.device)
-    _want(f, "xs", xs, (torch.float32,), (M, _cdiv(K, 128)), X.device)
-    _run(f, X.device, stream, (X.data_ptr(), _HALF[X.dtype], M, K, Xq.data_ptr(), xs.data_ptr()))
+    _want(f, "X", X, _HALF, (M, K), X.get_device())
+    _want(f, "Xq", Xq, _E4M3, (M, K), X.get_device())
+    _want(f, "xs", xs, (torch.float32,), (M, -(-K // 128)), X.get_device())
+    _run(f, X.get_device(), stream, (X.data_ptr(), _HALF[X.dtype], M, K, Xq.data_ptr(), xs.data_ptr()))
 
 
 def qg_quantize_weight_fp8(W, Wq, ws, stream=None):
@@ -390,11 +391,11 @@ def qg_quantize_weight_fp8(W, Wq, ws, stream=None):
     f = "qg_quantize_weight_fp8"
     _rank(f, "W", W, 2 if W.dim() == 2 else 3)
     K, N = W.shape[-2:]
-    _want(f, "W", W, _FLOAT, tuple(W.shape), W.device)
-    _want(f, "Wq", Wq, _E4M3, tuple(W.shape), W.device)
-    _want(f, "ws", ws, (torch.float32,), (*W.shape[:-2], _cdiv(K, 128), _cdiv(N, 128)), W.device)
+    _want(f, "W", W, _FLOAT, tuple(W.shape), W.get_device())
+    _want(f, "Wq", Wq, _E4M3, tuple(W.shape), W.get_device())
+    _want(f, "ws", ws, (torch.float32,), (*W.shape[:-2], -(-K // 128), -(-N // 128)), W.get_device())
     E = W.shape[0] if W.dim() == 3 else 1
-    _run(f, W.device, stream, (W.data_ptr(), _FLOAT[W.dtype], E, K, N, Wq.data_ptr(), ws.data_ptr()))
+    _run(f, W.get_device(), stream, (W.data_ptr(), _FLOAT[W.dtype], E, K, N, Wq.data_ptr(), ws.data_ptr()))
 
 
 def qg_gemm_fp8(Xq, xs, Wq, ws, Y, workspace="auto", stream=None):
@@ -402,12 +403,12 @@ def qg_gemm_fp8(Xq, xs, Wq, ws, Y, workspace="auto", stream=None):
     f = "qg_gemm_fp8"
     _rank(f, "Xq", Xq, 2)
     _rank(f, "Wq", Wq, 2)
-    (M, K), N, dev = Xq.shape, Wq.shape[1], Xq.device
-    G = _cdiv(K, 128)
+    (M, K), N, dev = Xq.shape, Wq.shape[1], Xq.get_device()
+    G = -(-K // 128)
     _want(f, "Xq", Xq, _E4M3, (M, K), dev)
     _want(f, "xs", xs, (torch.float32,), (M, G), dev)
     _want(f, "Wq", Wq, _E4M3, (K, N), dev)
-    _want(f, "ws", ws, (torch.float32,), (G, _cdiv(N, 128)), dev)
+    _want(f, "ws", ws, (torch.float32,), (G, -(-N // 128)), dev)
     _want(f, "Y", Y, _HALF, (M, N), dev)
     _run(f, dev, stream, (Xq.data_ptr(), xs.data_ptr(), M, K, Wq.data_ptr(), ws.data_ptr(), N, Y.data_ptr(),
                           _HALF[Y.dtype]), (QG_OP_GEMM_FP8, M, K, N), workspace)
@@ -421,7 +422,7 @@ def qg_route_topk(logits, bias, idx, weights, score="softmax", n_group=1, topk_g
         raise ValueError(f"{f}: score is {score!r}, not one of {', '.join(_SCORES)}")
     _rank(f, "logits", logits, 2)
     _rank(f, "idx", idx, 2)
-    (M, E), topk, dev = logits.shape, idx.shape[1], logits.device
+    (M, E), topk, dev = logits.shape, idx.shape[1], logits.get_device()
     _want(f, "logits", logits, _FLOAT, (M, E), dev)
     if bias is not None:
         _want(f, "bias", bias, (torch.float32,), (E,), dev)
@@ -437,7 +438,7 @@ def qg_expert_slots(idx, offsets, slot_token, token_slot, workspace="auto", stre
     f = "qg_expert_slots"
     _rank(f, "idx", idx, 2)
     _rank(f, "offsets", offsets, 1)
-    (M, topk), E, dev = idx.shape, offsets.shape[0] - 1, idx.device
+    (M, topk), E, dev = idx.shape, offsets.shape[0] - 1, idx.get_device()
     _want(f, "idx", idx, (torch.int32,), (M, topk), dev)
     _want(f, "offsets", offsets, (torch.int32,), (E + 1,), dev)
     _want(f, "slot_token", slot_token, (torch.int32,), (M * topk,), dev)
@@ -453,15 +454,15 @@ def qg_gemm_fp8_experts(Xq, xs, slot_token, offsets, Wq, ws, Y, workspace="auto"
     _rank(f, "Xq", Xq, 2)
     _rank(f, "Wq", Wq, 3)
     _rank(f, "Y", Y, 2)
-    (Mx, K), (E, _, N), S, dev = Xq.shape, Wq.shape, Y.shape[0], Xq.device
-    G = _cdiv(K, 128)
+    (Mx, K), (E, _, N), S, dev = Xq.shape, Wq.shape, Y.shape[0], Xq.get_device()
+    G = -(-K // 128)
     _want(f, "Xq", Xq, _E4M3, (Mx, K), dev)
     _want(f, "xs", xs, (torch.float32,), (Mx, G), dev)
     if slot_token is not None:
         _want(f, "slot_token", slot_token, (torch.int32,), (S,), dev)
     _want(f, "offsets", offsets, (torch.int32,), (E + 1,), dev)
     _want(f, "Wq", Wq, _E4M3, (E, K, N), dev)
-    _want(f, "ws", ws, (torch.float32,), (E, G, _cdiv(N, 128)), dev)
+    _want(f, "ws", ws, (torch.float32,), (E, G, -(-N // 128)), dev)
     _want(f, "Y", Y, _HALF, (S, N), dev)
     _run(f, dev, stream, (Xq.data_ptr(), xs.data_ptr(), Mx, K, None if slot_token is None else slot_token.data_ptr(),
                           offsets.data_ptr(), S, E, Wq.data_ptr(), ws.data_ptr(), N, Y.data_ptr(), _HALF[Y.dtype]),
@@ -473,7 +474,7 @@ def qg_combine_experts(D, token_slot, weights, Y, stream=None):
     f = "qg_combine_experts"
     _rank(f, "D", D, 2)
     _rank(f, "token_slot", token_slot, 2)
-    (S, N), (M, topk), dev = D.shape, token_slot.shape, D.device
+    (S, N), (M, topk), dev = D.shape, token_slot.shape, D.get_device()
     _want(f, "D", D, _HALF, (S, N), dev)
     _want(f, "token_slot", token_slot, (torch.int32,), (M, topk), dev)
     _want(f, "weights", weights, (torch.float32,), (M, topk), dev)

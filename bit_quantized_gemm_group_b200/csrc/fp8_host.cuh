@@ -144,7 +144,7 @@ bool slots_bad_shape(int M, int topk, int E)
 size_t slots_workspace(int M, int topk, int E)
 {
     const size_t blocks = ((size_t)M * topk + qg::kSlotBlock - 1) / qg::kSlotBlock;
-    return (blocks * E * sizeof(int32_t) + 255) / 256 * 256;
+    return blocks > 1 ? (blocks * E * sizeof(int32_t) + 255) / 256 * 256 : 0;
 }
 
 qg_status expert_slots(const int32_t* idx, int M, int topk, int E, int32_t* offsets, int32_t* slot_token,
@@ -155,14 +155,17 @@ qg_status expert_slots(const int32_t* idx, int M, int topk, int E, int32_t* offs
         QG_CUDA(cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (E + 1), st));
         return QG_OK;
     }
-    if (!workspace) return QG_ERR_NULL;
-    if (ws_bytes < slots_workspace(M, topk, E)) return QG_ERR_WORKSPACE;
+    const size_t need = slots_workspace(M, topk, E);
+    if (need && !workspace) return QG_ERR_NULL;
+    if (ws_bytes < need) return QG_ERR_WORKSPACE;
     const int n = M * topk, blocks = (n + qg::kSlotBlock - 1) / qg::kSlotBlock;
     const qg::SlotParams p{idx, offsets, slot_token, token_slot, static_cast<int32_t*>(workspace), n, topk, E, blocks};
-    qg::slot_count_kernel<<<blocks, 256, 0, st>>>(p);
-    qg::slot_place_kernel<<<blocks, 256, 0, st>>>(p);
-    QG_CUDA(cudaGetLastError());
-    return QG_OK;
+    const dim3 threads(32 * qg::kSlotWarps);
+    if (blocks > 1) {
+        const qg_status r = launch_pdl(qg::slot_count_kernel, dim3(blocks), threads, 0, stream, p);
+        if (r != QG_OK) return r;
+    }
+    return launch_pdl(qg::slot_place_kernel, dim3(blocks), threads, 0, stream, p);
 }
 
 qg_status combine_experts(const void* D, qg_dtype dt, int S, int N, const int32_t* token_slot, const float* weights,

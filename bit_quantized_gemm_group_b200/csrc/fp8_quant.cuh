@@ -28,7 +28,8 @@ QG_DEV_INLINE uint32_t e4m3x2(float lo, float hi)
 
 // The scale of a group from its largest magnitude; `q` divides by it.
 struct Fp8Scale {
-    float s;
+    float s, r;
+    bool plain;   // r may stand for the division
     QG_DEV_INLINE explicit Fp8Scale(float amax)
     {
         s = __fdiv_rn(amax, kE4M3Max);
@@ -36,8 +37,23 @@ struct Fp8Scale {
             set_status(5u);
             s = __int_as_float(0x7fffffff);
         }
+        plain = s > 0x1p-60f && s < 0x1p60f;   // no product below underflows or overflows
+        r = plain ? __frcp_rn(s) : 0.0f;
     }
     QG_DEV_INLINE float q(float x) const { return s > 0.0f ? __fdiv_rn(x, s) : 0.0f; }
+    // For x of at most 11 significant bits (fp16, bf16), where `plain`: a quotient that has the
+    // same e4m3 code as fp32(x / s).  Markstein's division: with r = fp32(1 / s) and the exact
+    // remainder x - q0 s, q0 + (x - q0 s) r is within 2^-23 of an ulp of x / s before it is rounded,
+    // so it can only differ from fp32(x / s) where x / s is that near to a midpoint of two fp32
+    // numbers, and the code only where that midpoint is next to a midpoint c (5 significant
+    // bits) of two e4m3 numbers.  x - c s is then a multiple of s's last bit times 2^-4, which
+    // forces s to within two last bits of a multiple of 1/8 and x = c k / 8, and then x / s is
+    // off that fp32 midpoint by more than the bound.  Three instructions for about ten.
+    QG_DEV_INLINE float quick(float x) const
+    {
+        const float q0 = __fmul_rn(x, r);
+        return fmaf(fmaf(-q0, s, x), r, q0);
+    }
 };
 
 template <int T>
@@ -78,10 +94,17 @@ __global__ void __launch_bounds__(256) quantize_act_fp8_kernel(const uint16_t* _
     if (l == 0) xs[id] = s.s;
     if (!in) return;
     uint32_t o[4];
+    if (s.plain) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        o[i] = e4m3x2(s.q(half_word<T>(w[2 * i], 0)), s.q(half_word<T>(w[2 * i], 1))) |
-               e4m3x2(s.q(half_word<T>(w[2 * i + 1], 0)), s.q(half_word<T>(w[2 * i + 1], 1))) << 16;
+        for (int i = 0; i < 4; ++i)
+            o[i] = e4m3x2(s.quick(half_word<T>(w[2 * i], 0)), s.quick(half_word<T>(w[2 * i], 1))) |
+                   e4m3x2(s.quick(half_word<T>(w[2 * i + 1], 0)), s.quick(half_word<T>(w[2 * i + 1], 1))) << 16;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = e4m3x2(s.q(half_word<T>(w[2 * i], 0)), s.q(half_word<T>(w[2 * i], 1))) |
+                   e4m3x2(s.q(half_word<T>(w[2 * i + 1], 0)), s.q(half_word<T>(w[2 * i + 1], 1))) << 16;
+    }
     *reinterpret_cast<uint4*>(Xq + at) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 

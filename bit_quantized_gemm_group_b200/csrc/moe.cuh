@@ -27,90 +27,80 @@ QG_DEV_INLINE float load_logit(const void* p, int64_t at)
 }
 
 // (key, index) order: larger key first, then lower index
-QG_DEV_INLINE bool before(double a, int i, double b, int j) { return a > b || (a == b && i < j); }
+template <typename T>
+QG_DEV_INLINE bool before(T a, int i, T b, int j) { return a > b || (a == b && i < j); }
 
-// One warp per token; lane l holds experts l, l + 32, ..  Scores and keys in binary64: which
-// of two nearly equal experts comes first is decided by the formula and not by rounding.
-template <int T, int VPL>
-__global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
+constexpr float kInf = __builtin_huge_valf();
+
+// The groups that stay, from the keys of the warp's token in shared memory (an expert that is not
+// available: -inf): a bit each.  `margin`: the least value that stays less the largest that goes.
+template <typename T>
+QG_DEV_INLINE uint32_t kept_groups(const T* key, const RouteParams& p, int lane, T* margin)
 {
-    __shared__ double skey[4][kMaxExperts];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int m = blockIdx.x * 4 + warp;
-    if (m >= p.M) return;
-    const int E = p.E;
-    double score[VPL], key[VPL];
-    bool bad = false, any = false;
-    float mx = -__int_as_float(0x7f800000);
-#pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-        const int e = lane + 32 * v;
-        const float x = e < E ? load_logit<T>(p.logits, (int64_t)m * E + e) : -__int_as_float(0x7f800000);
-        bad |= !(x < __int_as_float(0x7f800000));
-        any |= x > -__int_as_float(0x7f800000);
-        mx = fmaxf(mx, x);
-        score[v] = x;
+    const int size = p.E / p.n_group;
+    T top = -kInf;   // of group `lane`
+    if (lane < p.n_group) {
+        T a = -kInf, b = -kInf;
+        int i = lane % size;   // the lanes start apart: no bank conflicts where size is a multiple of 32
+        for (int n = 0; n < size; ++n) {
+            const T x = key[lane * size + i];
+            if (x > a) { b = a; a = x; }
+            else if (x > b) b = x;
+            if (++i == size) i = 0;
+        }
+        top = p.group_top == 2 && size > 1 ? a + b : a;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    any = __any_sync(0xffffffffu, any);
-    double sum = 0.0;
+    int rank = 0;   // groups that come before this one
+    for (int g = 0; g < p.n_group; ++g) rank += before(__shfl_sync(0xffffffffu, top, g), g, top, lane);
+    const bool in = lane < p.n_group && rank < p.topk_group;
+    const uint32_t last = __ballot_sync(0xffffffffu, lane < p.n_group && rank == p.topk_group - 1);
+    const uint32_t next = __ballot_sync(0xffffffffu, lane < p.n_group && rank == p.topk_group);
+    const T lo = __shfl_sync(0xffffffffu, top, __ffs(last) - 1);
+    *margin = next ? lo - __shfl_sync(0xffffffffu, top, __ffs(next) - 1) : (T)kInf;
+    if (*margin != *margin) *margin = 0;   // both -inf
+    return __ballot_sync(0xffffffffu, in);
+}
+
+// One token by one warp, straight from the definition: scores and keys in binary64 (which of
+// two nearly equal experts comes first is decided by the formula and not by rounding).  Lane l
+// holds experts l, l + 32, ..  x: the logits; `bad`: the token goes nowhere.
+template <int VPL>
+__device__ __noinline__ void route_exact(const RouteParams& p, const float (&x)[VPL], float mx, bool bad, double* skey, int m, int lane)
+{
+    const int E = p.E;
+    const bool any = mx > -kInf;
+    double score[VPL], key[VPL], sum = 0.0;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-        const double x = score[v];
-        key[v] = x;   // -inf stays -inf: not available
-        score[v] = !any ? 0.0 : p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)mx);
+        score[v] = !any ? 0.0 : p.sigmoid ? 1.0 / (1.0 + exp(-(double)x[v])) : exp((double)x[v] - (double)mx);
         sum += score[v];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const double lowest = -__longlong_as_double(0x7ff0000000000000ll);
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
         const int e = lane + 32 * v;
         if (!p.sigmoid && any) score[v] /= sum;
-        const bool there = key[v] > lowest;
-        const double b = p.bias && e < E ? (double)p.bias[e] : 0.0;
-        key[v] = there ? score[v] + b : lowest;
-        bad |= there && !(key[v] < -lowest);
-    }
-    if (__any_sync(0xffffffffu, bad)) {   // the token goes nowhere
-        if (lane == 0) set_status(5u);
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) key[v] = lowest;
+        key[v] = bad || !(x[v] > -kInf) ? -kInf : score[v] + (p.bias && e < E ? (double)p.bias[e] : 0.0);
     }
     if (p.n_group > 1) {
-        const int size = E / p.n_group;
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
-            if (lane + 32 * v < E) skey[warp][lane + 32 * v] = key[v];
+            if (lane + 32 * v < E) skey[lane + 32 * v] = key[v];
         __syncwarp();
-        double top = lowest;   // of group `lane`
-        if (lane < p.n_group) {
-            double a = lowest, b = lowest;
-            for (int i = 0; i < size; ++i) {
-                const double x = skey[warp][lane * size + i];
-                if (x > a) { b = a; a = x; }
-                else if (x > b) b = x;
-            }
-            top = p.group_top == 2 && size > 1 ? a + b : a;
-        }
-        int rank = 0;   // groups that come before this one
-        for (int g = 0; g < p.n_group; ++g) {
-            const double t = __shfl_sync(0xffffffffu, top, g);
-            rank += before(t, g, top, lane);
-        }
-        const uint32_t kept = __ballot_sync(0xffffffffu, lane < p.n_group && rank < p.topk_group);
+        double margin;
+        const uint32_t kept = kept_groups(skey, p, lane, &margin);
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
             const int e = lane + 32 * v;
-            if (e < E && !(kept >> (e / size) & 1u)) key[v] = lowest;
+            if (e < E && !(kept >> (e / (E / p.n_group)) & 1u)) key[v] = -kInf;
         }
+        __syncwarp();
     }
     double total = 0.0, wj = 0.0;
     int ej = -1;   // lane j keeps choice j
     for (int j = 0; j < p.topk; ++j) {
-        double k = lowest, sc = 0.0;
+        double k = -kInf, sc = 0.0;
         int i = kMaxExperts;
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
@@ -121,13 +111,12 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
             const int i2 = __shfl_xor_sync(0xffffffffu, i, o);
             if (before(k2, i2, k, i)) { k = k2; i = i2; sc = s2; }
         }
-        const bool there = k > lowest;
-        if (!there) { i = -1; sc = 0.0; }
+        if (!(k > -kInf)) { i = -1; sc = 0.0; }
         total += sc;
         if (lane == j) { ej = i; wj = sc; }
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
-            if (lane + 32 * v == i) key[v] = lowest;
+            if (lane + 32 * v == i) key[v] = -kInf;
     }
     if (lane < p.topk) {
         if (p.renorm) wj = total > 0.0 ? wj / total : 0.0;
@@ -136,10 +125,167 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
     }
 }
 
-// Slot maps: a counting sort of the M * topk choices by expert, then by token.  Blocks of
-// kSlotBlock choices; count: each block's choices per expert (a NULL hist: only block 0's,
-// kept in shared memory by place).
-constexpr int kSlotBlock = 1024;
+// fp32 keys as integers of the same order; 0: not available
+QG_DEV_INLINE uint32_t ordered(float x)
+{
+    const uint32_t b = __float_as_uint(x);
+    return x > -kInf ? b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u) : 0u;
+}
+QG_DEV_INLINE float unordered(uint32_t u) { return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
+
+// One warp per token.  Without a bias the choice is by the logits (both scores rise with them);
+// with one, and for groups, by fp32 keys.  Where fp32 cannot tell an order that binary64 decides
+// -- two keys, or the last group kept and the first dropped, nearer than the keys' error;
+// logits that binary64 scores cannot tell apart (saturated, or nearer than 2^-40) -- the token
+// is done again by route_exact: about one in a hundred of 256 experts with a bias.  The
+// weights of the choices are computed in binary64 either way, one lane each.
+// Bound by the choice: 8 + 1 rounds of a maximum over the warp (16384 x 256, bias and groups).
+template <int T, int VPL>
+__global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
+{
+    __shared__ double skey[4][kMaxExperts];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int m = blockIdx.x * 4 + warp;
+    if (m >= p.M) return;
+    const int E = p.E;
+    float x[VPL], key[VPL], mx = -kInf;
+    bool bad = false;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+        const int e = lane + 32 * v;
+        x[v] = e < E ? load_logit<T>(p.logits, (int64_t)m * E + e) : -kInf;
+        bad |= !(x[v] < kInf);
+        mx = fmaxf(mx, x[v]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (p.bias) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const int e = lane + 32 * v;
+            const float b = e < E ? __ldg(p.bias + e) : 0.0f;
+            bad |= x[v] > -kInf && !(b < kInf);
+            key[v] = b;
+        }
+    }
+    if (__any_sync(0xffffffffu, bad)) {   // the token goes nowhere
+        if (lane == 0) set_status(5u);
+        route_exact<VPL>(p, x, -kInf, true, skey[warp], m, lane);
+        return;
+    }
+    // fp32 scores, where they are needed: each is within 2^-20 of its value
+    double sum = 0.0;
+    const bool scores = p.bias || p.n_group > 1;
+    if (scores || (!p.sigmoid && !p.renorm)) {
+        float sc[VPL];
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            sc[v] = p.sigmoid ? __frcp_rn(1.0f + expf(-x[v])) : mx > -kInf ? expf(x[v] - mx) : 0.0f;
+            sum += sc[v];
+        }
+        float inv = 1.0f;
+        if (!p.sigmoid) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            inv = sum > 0.0 ? 1.0f / (float)sum : 0.0f;
+        }
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) key[v] = fmaf(sc[v], inv, p.bias ? key[v] : 0.0f);
+    }
+    float far = 1.0f;   // the keys' largest magnitude
+    if (scores) {
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            if (!(x[v] > -kInf)) key[v] = -kInf;
+            if (key[v] > -kInf) far = fmaxf(far, fabsf(key[v]));
+        }
+        far = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(far)));
+    }
+    const float near = 0x1p-17f * far;   // two keys nearer than this may be the other way round
+    bool again = p.sigmoid && mx > 16.0f;
+    uint32_t u[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) u[v] = ordered(p.bias ? key[v] : x[v]);
+    if (p.n_group > 1) {
+        float* fkey = reinterpret_cast<float*>(skey[warp]);
+        __syncwarp();
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            if (lane + 32 * v < E) fkey[lane + 32 * v] = key[v];
+        __syncwarp();
+        float margin;
+        const uint32_t kept = kept_groups(fkey, p, lane, &margin);
+        again |= margin <= 2.0f * near;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+            const int e = lane + 32 * v;
+            if (e < E && !(kept >> (e / (E / p.n_group)) & 1u)) u[v] = 0u;
+        }
+        __syncwarp();
+    }
+    int ej = -1;   // lane j keeps choice j
+    float xj = -kInf;
+    uint32_t prev = 0u;
+    for (int j = 0; j <= p.topk && !again; ++j) {   // one further, to see how near it is
+        uint32_t best = u[0];
+#pragma unroll
+        for (int v = 1; v < VPL; ++v) best = max(best, u[v]);
+        best = __reduce_max_sync(0xffffffffu, best);
+        if (j > 0 && best > 0u) {
+            const float gap = unordered(prev) - unordered(best);
+            again = p.bias ? gap <= near : gap > 0.0f && gap < 0x1p-40f;
+        }
+        if (best == 0u || j == p.topk) break;
+        // the lowest expert of that key
+        int i = kMaxExperts;
+#pragma unroll
+        for (int v = VPL - 1; v >= 0; --v)
+            if (u[v] == best) i = lane + 32 * v;
+        i = __reduce_min_sync(0xffffffffu, i);
+        float xi = -kInf;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+            if (lane + 32 * v == i) {
+                xi = x[v];
+                u[v] = 0u;
+            }
+        xi = __shfl_sync(0xffffffffu, xi, i & 31);
+        if (lane == j) {
+            ej = i;
+            xj = xi;
+        }
+        prev = best;
+        // scores that binary64 has as 0 or subnormal
+        again |= p.sigmoid ? xi < -600.0f : xi - mx < -600.0f;
+    }
+    if (again) {
+        route_exact<VPL>(p, x, mx, false, skey[warp], m, lane);
+        return;
+    }
+    double w = 0.0;
+    if (ej >= 0) w = p.sigmoid ? 1.0 / (1.0 + exp(-(double)xj)) : exp((double)xj - (double)mx);
+    if (p.renorm) {
+        double total = w;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        w = total > 0.0 ? w / total : 0.0;
+    } else if (!p.sigmoid && ej >= 0) {
+        w /= sum;
+    }
+    if (lane < p.topk) {
+        p.idx[(int64_t)m * p.topk + lane] = ej;
+        p.weights[(int64_t)m * p.topk + lane] = (float)(w * (double)p.scale);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Slot maps: a stable counting sort of the M * topk choices by expert.  Blocks of kSlotBlock
+// choices, 128 for each warp in four rounds: in a round the lanes of equal choices find one
+// another (match), so a choice's rank is the warp's count so far plus the lanes before it;
+// then the warps' counts are summed up, and the blocks' (slot_count_kernel's, unless there is
+// but one).  Latency-bound: a launch and a handful of dependent steps each.
+// ---------------------------------------------------------------------------
+constexpr int kSlotBlock = 4096, kSlotWarps = 32;
 
 struct SlotParams {
     const int32_t* idx;   // [n]
@@ -150,63 +296,108 @@ struct SlotParams {
     int n, topk, E, blocks;
 };
 
-__global__ void __launch_bounds__(256) slot_count_kernel(const SlotParams p)
+__global__ void __launch_bounds__(32 * kSlotWarps) slot_count_kernel(const SlotParams p)
 {
     __shared__ int cnt[kMaxExperts];
-    for (int e = threadIdx.x; e < p.E; e += 256) cnt[e] = 0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) cnt[e] = 0;
     __syncthreads();
     const int end = min(p.n, ((int)blockIdx.x + 1) * kSlotBlock);
-    for (int i = blockIdx.x * kSlotBlock + threadIdx.x; i < end; i += 256) {
+    for (int i = blockIdx.x * kSlotBlock + threadIdx.x; i < end; i += blockDim.x) {
         const int e = p.idx[i];
         if (e >= 0 && e < p.E) atomicAdd(&cnt[e], 1);
-        else if (e != -1) set_status(6u);   // not an expert: left out, like -1
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += 256) p.hist[blockIdx.x * p.E + e] = cnt[e];
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.hist[blockIdx.x * p.E + e] = cnt[e];
 }
 
-__global__ void __launch_bounds__(256) slot_place_kernel(const SlotParams p)
+__global__ void __launch_bounds__(32 * kSlotWarps) slot_place_kernel(const SlotParams p)
 {
-    __shared__ int base[kMaxExperts];    // slots before this block's first of each expert
+    __shared__ uint16_t wcnt[kSlotWarps][kMaxExperts];   // the warps' choices, then those of the warps before
+    __shared__ int base[kMaxExperts];                    // this block's first slot of each expert
     __shared__ int total[kMaxExperts];
-    __shared__ int chunk[kSlotBlock];
-    for (int e = threadIdx.x; e < p.E; e += 256) {
-        int b = 0, t = 0;
-        for (int k = 0; k < p.blocks; ++k) {
-            const int c = p.hist[k * p.E + e];
-            b += k < (int)blockIdx.x ? c : 0;
-            t += c;
+    __shared__ int used_s;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i0 = blockIdx.x * kSlotBlock + warp * 128 + lane;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    for (int e = lane; e < p.E; e += 32) wcnt[warp][e] = 0;
+    __syncwarp();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int e[4], rank[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = i0 + 32 * r;
+        e[r] = i < p.n ? p.idx[i] : -1;
+        if ((uint32_t)e[r] >= (uint32_t)p.E) {
+            if (e[r] != -1) set_status(6u);   // not an expert: left out, like -1
+            e[r] = -1;
         }
-        base[e] = b;
-        total[e] = t;
     }
-    const int i0 = blockIdx.x * kSlotBlock, cnt = min(kSlotBlock, p.n - i0);
-    for (int i = threadIdx.x; i < cnt; i += 256) chunk[i] = p.idx[i0 + i];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const uint32_t same = __match_any_sync(0xffffffffu, e[r]);
+        const int ahead = __popc(same & ((1u << lane) - 1u));
+        rank[r] = 0;
+        if (e[r] >= 0) rank[r] = wcnt[warp][e[r]] + ahead;
+        __syncwarp();
+        if (e[r] >= 0 && ahead == 0) wcnt[warp][e[r]] += __popc(same);
+        __syncwarp();
+    }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        int at = 0;
-        for (int e = 0; e < p.E; ++e) {
-            base[e] += at;
-            if (blockIdx.x == 0) p.offsets[e] = at;
-            at += total[e];
+    for (int x = threadIdx.x; x < p.E; x += blockDim.x) {
+        int n = 0;
+#pragma unroll 8
+        for (int w = 0; w < kSlotWarps; ++w) {
+            const int c = wcnt[w][x];
+            wcnt[w][x] = n;
+            n += c;
         }
-        if (blockIdx.x == 0) p.offsets[p.E] = at;
-        total[0] = at;
+        int b = 0, t = n;
+        if (p.blocks > 1) {
+            t = 0;
+#pragma unroll 8
+            for (int k = 0; k < p.blocks; ++k) {
+                const int c = __ldcg(p.hist + k * p.E + x);
+                b += k < (int)blockIdx.x ? c : 0;
+                t += c;
+            }
+        }
+        base[x] = b;
+        total[x] = t;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < cnt; i += 256) {
-        const int e = chunk[i];
-        int slot = -1;
-        if (e >= 0 && e < p.E) {
-            slot = base[e];
-            for (int j = 0; j < i; ++j) slot += chunk[j] == e;
-            p.slot_token[slot] = (i0 + i) / p.topk;
+    if (warp == 0) {   // the experts' first slots
+        int run = 0;
+        for (int x0 = 0; x0 < p.E; x0 += 32) {
+            const int x = x0 + lane, t = x < p.E ? total[x] : 0;
+            int v = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int a = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += a;
+            }
+            if (x < p.E) {
+                base[x] += run + v - t;
+                if (blockIdx.x == 0) p.offsets[x] = run + v - t;
+            }
+            run += __shfl_sync(0xffffffffu, v, 31);
         }
-        p.token_slot[i0 + i] = slot;
+        if (lane == 0) {
+            used_s = run;
+            if (blockIdx.x == 0) p.offsets[p.E] = run;
+        }
     }
-    const int used = total[0];   // entries without a choice
-    for (int i = i0 + threadIdx.x; i < i0 + cnt; i += 256)
-        if (i >= used) p.slot_token[i] = -1;
+    __syncthreads();
+    const int used = used_s;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int i = i0 + 32 * r;
+        if (i >= p.n) continue;
+        const int slot = e[r] >= 0 ? base[e[r]] + wcnt[warp][e[r]] + rank[r] : -1;
+        if (slot >= 0) p.slot_token[slot] = i / p.topk;
+        p.token_slot[i] = slot;
+        if (i >= used) p.slot_token[i] = -1;   // entries without a choice
+    }
 }
 
 // Y[m] = rn( sum_j weights[m][j] D[token_slot[m][j]] ), j in order, fp32.  One thread per 8
