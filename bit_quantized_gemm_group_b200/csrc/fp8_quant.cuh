@@ -162,9 +162,11 @@ __global__ void __launch_bounds__(512) quantize_weight_fp8_kernel(const void* __
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + 16 * i;
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = T != IN_F32 && s.plain ? s.quick(v[i][j]) : s.q(v[i][j]);
         if (r < K && c < N)
-            *reinterpret_cast<uint32_t*>(Wq + (e * K + r) * N + c) =
-                e4m3x2(s.q(v[i][0]), s.q(v[i][1])) | e4m3x2(s.q(v[i][2]), s.q(v[i][3])) << 16;
+            *reinterpret_cast<uint32_t*>(Wq + (e * K + r) * N + c) = e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16;
     }
 }
 

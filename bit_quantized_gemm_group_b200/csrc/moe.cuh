@@ -38,18 +38,29 @@ template <typename T>
 QG_DEV_INLINE uint32_t kept_groups(const T* key, const RouteParams& p, int lane, T* margin)
 {
     const int size = p.E / p.n_group;
-    T top = -kInf;   // of group `lane`
-    if (lane < p.n_group) {
-        T a = -kInf, b = -kInf;
-        int i = lane % size;   // the lanes start apart: no bank conflicts where size is a multiple of 32
-        for (int n = 0; n < size; ++n) {
-            const T x = key[lane * size + i];
+    // `sub` lanes a group (32 over n_group rounded up to a power of two), each every sub-th
+    // expert; the lanes start apart, so that groups of 32 do not meet in a bank
+    const int log = p.n_group > 1 ? 32 - __clz(p.n_group - 1) : 0, sub = 32 >> log, g = lane >> (5 - log);
+    T a = -kInf, b = -kInf;
+    if (g < p.n_group) {
+        int i = lane % size;
+        const int own = lane & (sub - 1);
+        for (int n = own; n < size; n += sub) {
+            const T x = key[g * size + i];
             if (x > a) { b = a; a = x; }
             else if (x > b) b = x;
-            if (++i == size) i = 0;
+            i += sub;
+            while (i >= size) i -= size;
         }
-        top = p.group_top == 2 && size > 1 ? a + b : a;
     }
+    for (int o = 1; o < sub; o <<= 1) {
+        const T a2 = __shfl_xor_sync(0xffffffffu, a, o), b2 = __shfl_xor_sync(0xffffffffu, b, o);
+        b = a > a2 ? (b > a2 ? b : a2) : (a > b2 ? a : b2);
+        a = a > a2 ? a : a2;
+    }
+    T top = p.group_top == 2 && size > 1 ? a + b : a;
+    top = __shfl_sync(0xffffffffu, top, (lane << (5 - log)) & 31);   // lane g: group g's value
+    if (lane >= p.n_group) top = -kInf;
     int rank = 0;   // groups that come before this one
     for (int g = 0; g < p.n_group; ++g) rank += before(__shfl_sync(0xffffffffu, top, g), g, top, lane);
     const bool in = lane < p.n_group && rank < p.topk_group;
@@ -63,12 +74,15 @@ QG_DEV_INLINE uint32_t kept_groups(const T* key, const RouteParams& p, int lane,
 
 // One token by one warp, straight from the definition: scores and keys in binary64 (which of
 // two nearly equal experts comes first is decided by the formula and not by rounding).  Lane l
-// holds experts l, l + 32, ..  x: the logits; `bad`: the token goes nowhere.
-template <int VPL>
-__device__ __noinline__ void route_exact(const RouteParams& p, const float (&x)[VPL], float mx, bool bad, double* skey, int m, int lane)
+// holds experts l, l + 32, ..  mx: the largest logit; `bad`: the token goes nowhere.
+template <int T, int VPL>
+__device__ __noinline__ void route_exact(const RouteParams& p, float mx, bool bad, double* skey, int m, int lane)
 {
     const int E = p.E;
     const bool any = mx > -kInf;
+    float x[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) x[v] = lane + 32 * v < E ? load_logit<T>(p.logits, (int64_t)m * E + lane + 32 * v) : -kInf;
     double score[VPL], key[VPL], sum = 0.0;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
@@ -97,26 +111,37 @@ __device__ __noinline__ void route_exact(const RouteParams& p, const float (&x)[
         }
         __syncwarp();
     }
+    unsigned long long u[VPL];   // the keys as integers of the same order; 0: not available
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+        const unsigned long long bits = __double_as_longlong(key[v] + 0.0);   // -0 is 0
+        u[v] = key[v] > -kInf ? bits ^ ((bits >> 63) ? ~0ull : 1ull << 63) : 0ull;
+    }
     double total = 0.0, wj = 0.0;
     int ej = -1;   // lane j keeps choice j
     for (int j = 0; j < p.topk; ++j) {
-        double k = -kInf, sc = 0.0;
-        int i = kMaxExperts;
+        unsigned long long best = u[0];
+#pragma unroll
+        for (int v = 1; v < VPL; ++v) best = max(best, u[v]);
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
+        const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+        best = (unsigned long long)hi << 32 | lo;
+        if (best == 0ull) break;
+        int i = kMaxExperts;   // the lowest expert of that key
+#pragma unroll
+        for (int v = VPL - 1; v >= 0; --v)
+            if (u[v] == best) i = lane + 32 * v;
+        i = __reduce_min_sync(0xffffffffu, i);
+        double sc = 0.0;
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
-            if (before(key[v], lane + 32 * v, k, i)) { k = key[v]; i = lane + 32 * v; sc = score[v]; }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const double k2 = __shfl_xor_sync(0xffffffffu, k, o), s2 = __shfl_xor_sync(0xffffffffu, sc, o);
-            const int i2 = __shfl_xor_sync(0xffffffffu, i, o);
-            if (before(k2, i2, k, i)) { k = k2; i = i2; sc = s2; }
-        }
-        if (!(k > -kInf)) { i = -1; sc = 0.0; }
+            if (lane + 32 * v == i) {
+                sc = score[v];
+                u[v] = 0ull;
+            }
+        sc = __shfl_sync(0xffffffffu, sc, i & 31);
         total += sc;
         if (lane == j) { ej = i; wj = sc; }
-#pragma unroll
-        for (int v = 0; v < VPL; ++v)
-            if (lane + 32 * v == i) key[v] = -kInf;
     }
     if (lane < p.topk) {
         if (p.renorm) wj = total > 0.0 ? wj / total : 0.0;
@@ -128,7 +153,7 @@ __device__ __noinline__ void route_exact(const RouteParams& p, const float (&x)[
 // fp32 keys as integers of the same order; 0: not available
 QG_DEV_INLINE uint32_t ordered(float x)
 {
-    const uint32_t b = __float_as_uint(x);
+    const uint32_t b = __float_as_uint(x + 0.0f);   // -0 is 0
     return x > -kInf ? b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u) : 0u;
 }
 QG_DEV_INLINE float unordered(uint32_t u) { return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
@@ -137,8 +162,7 @@ QG_DEV_INLINE float unordered(uint32_t u) { return __uint_as_float(u ^ ((u >> 31
 // with one, and for groups, by fp32 keys.  Where fp32 cannot tell an order that binary64 decides
 // -- two keys, or the last group kept and the first dropped, nearer than the keys' error;
 // logits that binary64 scores cannot tell apart (saturated, or nearer than 2^-40) -- the token
-// is done again by route_exact: about one in a hundred of 256 experts with a bias.  The
-// weights of the choices are computed in binary64 either way, one lane each.
+// is done again by route_exact: about one in two hundred of 256 experts with a bias.
 // Bound by the choice: 8 + 1 rounds of a maximum over the warp (16384 x 256, bias and groups).
 template <int T, int VPL>
 __global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
@@ -170,7 +194,7 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
     }
     if (__any_sync(0xffffffffu, bad)) {   // the token goes nowhere
         if (lane == 0) set_status(5u);
-        route_exact<VPL>(p, x, -kInf, true, skey[warp], m, lane);
+        route_exact<T, VPL>(p, -kInf, true, skey[warp], m, lane);
         return;
     }
     // fp32 scores, where they are needed: each is within 2^-20 of its value
@@ -181,7 +205,7 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
             sc[v] = p.sigmoid ? __frcp_rn(1.0f + expf(-x[v])) : mx > -kInf ? expf(x[v] - mx) : 0.0f;
-            sum += sc[v];
+            if (!p.sigmoid) sum += sc[v];
         }
         float inv = 1.0f;
         if (!p.sigmoid) {
@@ -201,7 +225,9 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
         }
         far = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(far)));
     }
-    const float near = 0x1p-17f * far;   // two keys nearer than this may be the other way round
+    // two keys nearer than this may be the other way round: a score is within 2^-21 (expf, the sum
+    // and the quotient, each a few 2^-24 of at most 1), a key within 2^-24 of itself more
+    const float near = 0x1p-19f * far;
     bool again = p.sigmoid && mx > 16.0f;
     uint32_t u[VPL];
 #pragma unroll
@@ -224,7 +250,6 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
         __syncwarp();
     }
     int ej = -1;   // lane j keeps choice j
-    float xj = -kInf;
     uint32_t prev = 0u;
     for (int j = 0; j <= p.topk && !again; ++j) {   // one further, to see how near it is
         uint32_t best = u[0];
@@ -241,40 +266,42 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
 #pragma unroll
         for (int v = VPL - 1; v >= 0; --v)
             if (u[v] == best) i = lane + 32 * v;
-        i = __reduce_min_sync(0xffffffffu, i);
-        float xi = -kInf;
+        const uint32_t who = __ballot_sync(0xffffffffu, i < kMaxExperts);
+        i = (who & (who - 1u)) ? __reduce_min_sync(0xffffffffu, i) : __shfl_sync(0xffffffffu, i, __ffs(who) - 1);
 #pragma unroll
         for (int v = 0; v < VPL; ++v)
-            if (lane + 32 * v == i) {
-                xi = x[v];
-                u[v] = 0u;
-            }
-        xi = __shfl_sync(0xffffffffu, xi, i & 31);
-        if (lane == j) {
-            ej = i;
-            xj = xi;
-        }
+            if (lane + 32 * v == i) u[v] = 0u;
+        if (lane == j) ej = i;
         prev = best;
-        // scores that binary64 has as 0 or subnormal
-        again |= p.sigmoid ? xi < -600.0f : xi - mx < -600.0f;
     }
+    const float xj = ej >= 0 ? load_logit<T>(p.logits, (int64_t)m * E + ej) : -kInf;
+    // scores that are small for fp32 (and their sum), or 0 in binary64
+    again |= __any_sync(0xffffffffu, ej >= 0 && (p.sigmoid ? xj : xj - mx) < -60.0f);
     if (again) {
-        route_exact<VPL>(p, x, mx, false, skey[warp], m, lane);
+        route_exact<T, VPL>(p, mx, false, skey[warp], m, lane);
         return;
     }
-    double w = 0.0;
-    if (ej >= 0) w = p.sigmoid ? 1.0 / (1.0 + exp(-(double)xj)) : exp((double)xj - (double)mx);
+    float w = 0.0f;   // within 16 * 2^-24 of its value in all
+    if (ej >= 0) {
+        if (p.sigmoid) {
+            w = __frcp_rn(1.0f + expf(-xj));
+        } else {   // exp of the exact difference: d and what its rounding left out
+            const float d = xj - mx, t = d - xj, left = (xj - (d - t)) + (-mx - t);
+            w = expf(d);
+            w = fmaf(w, left, w);
+        }
+    }
     if (p.renorm) {
-        double total = w;
+        float total = w;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        w = total > 0.0 ? w / total : 0.0;
+        w = total > 0.0f ? __fdiv_rn(w, total) : 0.0f;
     } else if (!p.sigmoid && ej >= 0) {
-        w /= sum;
+        w = (float)((double)w / sum);
     }
     if (lane < p.topk) {
         p.idx[(int64_t)m * p.topk + lane] = ej;
-        p.weights[(int64_t)m * p.topk + lane] = (float)(w * (double)p.scale);
+        p.weights[(int64_t)m * p.topk + lane] = w * p.scale;
     }
 }
 
