@@ -209,7 +209,7 @@ QG_DEV_INLINE void fp8_fold(float (&acc)[CW], uint32_t addr, float sc, F release
 // 4096, 4 rows (86 steps down to 19): 27.5 -> 17.1 us; K = 4096 (32 down to 7): 11.8 -> 13.8 us,
 // left whole; K = 11008 with 128 rows: no difference.
 constexpr int kFp8MinUnits = 4;   // of a piece
-QG_DEV_INLINE int fp8_min_saved(int rows) { return 34 + rows / 4; }
+__host__ __device__ inline int fp8_min_saved(int rows) { return 34 + rows / 4; }
 
 struct Fp8Work {   // in shared memory: the folding threads have no registers to spare
     int G, grid, cta;
@@ -327,6 +327,7 @@ struct Fp8TileCfg {
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128, STAGE = A_BYTES + B_BYTES;
     static constexpr int ST = BN == 256 ? 4 : 6;          // even: a stage always serves the same issuer
     static constexpr int THREADS = 384, TMEM_COLS = DB * BN;
+    static constexpr int REGS_ISSUE = 72, REGS_FOLD = 216;   // after the split: of warps 0..3 and 4..11
     static constexpr int OUT_OFF = ST * STAGE;            // per fold warp: 32 rows x 32 columns of Y
     static constexpr int SCHED_OFF = OUT_OFF + 8 * 32 * 64;
     static constexpr int BAR_OFF = SCHED_OFF + (int)((sizeof(Fp8Sched) + 15) / 16 * 16);
@@ -431,7 +432,7 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
     const uint32_t tmem = *tslot;
 
     if (warp < 4) {
-        setmaxnreg_dec<72>();
+        setmaxnreg_dec<C::REGS_ISSUE>();
         if (warp == 0) {
             // ---------------- producer ----------------
             Fp8Walk<C::BM> walk(sched, p.E, slabs);
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
             }
         }
     } else {
-        setmaxnreg_inc<216>();
+        setmaxnreg_inc<C::REGS_FOLD>();
         // ---------------- fold: thread = row, HW columns ----------------
         const int q = warp & 3, half = (warp - 4) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16) + half * HW;

@@ -33,8 +33,12 @@ qg_status quantize_weight_fp8(const void* W, int E, int K, int N, uint8_t* Wq, f
 // ---------------------------------------------------------------------------
 bool fp8_bad_shape(int K, int N) { return K < 16 || K % 16 || N < 16 || N % 16; }
 
-// The workspace: counters and partial sums of split tiles, then (mapped rows) the rows in slot
-// order.  256 columns a tile are assumed: the number of experts, and so the choice, is not known.
+// Rows of a TMA box of activations: what a tile can have.
+int fp8_box(int S) { return S >= 128 ? 128 : (S + 7) / 8 * 8; }
+
+// The workspace: counters and partial sums of split tiles (where K is long enough to be split),
+// then, for experts, the rows in slot order.  256 columns a tile are assumed: the number of
+// experts, and so the choice, is not known.
 struct Fp8Workspace {
     size_t partials, rows, bytes;   // where the second and third part start, and all
 };
@@ -42,14 +46,32 @@ struct Fp8Workspace {
 Fp8Workspace fp8_carve(int S, int K, bool experts)
 {
     const size_t grid = num_sms();
+    const bool split = (K + 127) / 128 > qg::fp8_min_saved(fp8_box(S));
     Fp8Workspace w;
     w.partials = (grid * 8 + 255) / 256 * 256;
-    w.rows = w.partials + grid * 2 * 128 * 256 * sizeof(float);
+    w.rows = split ? w.partials + grid * 2 * 128 * 256 * sizeof(float) : 0;
     w.bytes = w.rows + (experts ? (size_t)S * K : 0);
     return w;
 }
 
 size_t fp8_workspace(int S, int K, bool experts) { return fp8_carve(S, K, experts).bytes; }
+
+// The kernel's register split draws on what the block was launched with: a build that gives it
+// fewer would wait for ever.
+template <typename C, typename Kern>
+qg_status fp8_check_registers(Kern kern)
+{
+    static std::atomic<int> fine{0};
+    if (fine.load(std::memory_order_relaxed)) return QG_OK;
+    cudaFuncAttributes a;
+    QG_CUDA(cudaFuncGetAttributes(&a, kern));
+    if (a.numRegs * C::THREADS < 128 * C::REGS_ISSUE + 256 * C::REGS_FOLD) {
+        snprintf(g_last_error, sizeof(g_last_error), "FP8 tile kernel built with %d registers a thread", a.numRegs);
+        return QG_ERR_UNSUPPORTED;
+    }
+    fine.store(1, std::memory_order_relaxed);
+    return QG_OK;
+}
 
 // The weights as {N, K, E} (boxes of 128 columns x 128 k), the activations as {K, rows} (boxes of
 // 128 k x p.box rows).
@@ -70,8 +92,8 @@ qg_status launch_fp8_tile(qg::Fp8Params p, const uint8_t* X, const uint8_t* Wq, 
     static KernelInfo info;
     int occ = 1;
     qg_status st = prepare_kernel(info, kern, C::THREADS, C::TOTAL, &occ);
-    if (st != QG_OK) return st;
-    const Fp8Workspace w = fp8_carve(p.S, p.K, p.rows != nullptr);
+    if (st != QG_OK || (st = fp8_check_registers<C>(kern)) != QG_OK) return st;
+    const Fp8Workspace w = fp8_carve(p.S, p.K, p.offsets != nullptr);
     uint8_t* base = static_cast<uint8_t*>(ws);
     p.counters = reinterpret_cast<unsigned long long*>(base);
     p.partials = reinterpret_cast<float*>(base + w.partials);
@@ -93,11 +115,12 @@ qg_status fp8_gemm(const uint8_t* Xq, const float* xs, int Mx, int K, const int3
                    int E, const uint8_t* Wq, const float* ws, int N, void* Y, qg_dtype ydt, void* workspace,
                    size_t ws_bytes, qg_stream_t stream)
 {
-    if (!Xq || !xs || !Wq || !ws || !Y || !workspace) return QG_ERR_NULL;
+    const size_t need = fp8_workspace(S, K, offsets != nullptr);
+    if (!Xq || !xs || !Wq || !ws || !Y || (need && !workspace)) return QG_ERR_NULL;
     if (misaligned(Xq) || misaligned(xs) || misaligned(rows) || misaligned(offsets) || misaligned(Wq) ||
         misaligned(ws) || misaligned(Y) || misaligned(workspace))
         return QG_ERR_ALIGN;
-    if (ws_bytes < fp8_workspace(S, K, offsets != nullptr)) return QG_ERR_WORKSPACE;
+    if (ws_bytes < need) return QG_ERR_WORKSPACE;
     qg::Fp8Params p{};
     p.xs = xs;
     p.ws = ws;
@@ -112,7 +135,7 @@ qg_status fp8_gemm(const uint8_t* Xq, const float* xs, int Mx, int K, const int3
     p.G = (K + 127) / 128;
     p.NB = (N + 127) / 128;
     p.bf16 = ydt == QG_BF16;
-    p.box = S >= 128 ? 128 : (S + 7) / 8 * 8;   // the rest of a tile holds what it held: rows of sums that go nowhere
+    p.box = fp8_box(S);   // the rest of a tile holds what it held: rows of sums that go nowhere
     // 256 columns a tile where those tiles still fill half of the GPU
     const int64_t m_tiles = (int64_t)(S + 127) / 128 + (offsets ? std::min(S, E) / 2 : 0);
     if (m_tiles * ((N + 255) / 256) * 2 < num_sms()) return launch_fp8_tile<128>(p, Xq, Wq, workspace, stream);

@@ -262,11 +262,37 @@ def test_gemm_any_scales():
     assert_product(product(Xq, xs, Wq, ws), *values(Xq, xs, Wq, ws))
 
 
+# long K, where tiles are split and joined: one piece's worth to all of a tile's rows, both tile
+# widths (the last two), and whole waves of tiles before the split ones (the last)
+SPLIT = [(1, 11008, 4096), (5, 8320, 16), (17, 11008, 400), (64, 12304, 1040), (128, 28672, 128), (130, 12800, 272),
+         (3, 16384, 20480), (2, 6144, 38416)]
+
+
+@pytest.mark.parametrize("M,K,N", SPLIT)
+def test_gemm_split_exact(M, K, N):
+    o = exact_operands(M, K, N, M + N)
+    x, w = values(*o)
+    want = (x @ w).to(torch.bfloat16)
+    for _ in range(3):
+        assert torch.equal(product(*o), want)
+    assert q.qg_device_status() == q.QG_OK
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 11008, 4096), (64, 12304, 1040)])
+def test_gemm_split_rounds_once_and_the_same_every_time(M, K, N):
+    o = operands(M, K, N, 3)
+    Y = product(*o, dtype=torch.float16)
+    assert_product(Y, *values(*o))
+    for _ in range(20):
+        assert torch.equal(product(*o, dtype=torch.float16).view(torch.int16), Y.view(torch.int16))
+
+
 def test_gemm_workspace_contents_do_not_matter():
-    for M, K, N in ((1, 4096, 4096), (33, 4096, 4112), (300, 2048, 1040)):
+    for M, K, N in ((1, 11008, 4096), (33, 8192, 272), (100, 28672, 128)):
         o = operands(M, K, N, 7)
         want = product(*o)
         need = q.qg_workspace_size(q.QG_OP_GEMM_FP8, M, K, N)
+        assert need > 0
         for fill in (0, 0xFF, 0x5A):
             ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
             for _ in range(2):
@@ -275,12 +301,12 @@ def test_gemm_workspace_contents_do_not_matter():
 
 def test_gemm_on_another_stream_and_two_graphs():
     """Two captured graphs replayed in turn and at once, and an eager call on a stream of its own."""
-    sets = [operands(M, 4096, 4112, 20 + M) for M in (3, 40)]
+    sets = [operands(M, 11008, 528, 20 + M) for M in (3, 40)]   # tiles of both are split
     want = [product(*o) for o in sets]
     torch.cuda.synchronize()
     graphs, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
     for o in sets:
-        Y = torch.full((o[0].shape[0], 4112), NAN, dtype=torch.bfloat16, device="cuda")
+        Y = torch.full((o[0].shape[0], 528), NAN, dtype=torch.bfloat16, device="cuda")
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             q.qg_gemm_fp8(*o, Y)
@@ -393,8 +419,23 @@ def test_experts_bad_maps(counts):
         assert q.qg_device_status() == q.QG_ERR_RANGE and torch.isnan(Y).all()
 
 
+@pytest.mark.parametrize("counts", [[1, 0, 2], [0, 70, 0, 3], [1] * 20, [9, 0, 0, 160]])
+def test_experts_split_exact(counts):
+    """Long K: the last experts' tiles are split along it."""
+    Xq, xs, tok, off, Wq, ws = expert_operands(40, len(counts), 11008, 528, counts, 4, exact=True)
+    want = torch.cat([(lambda x, w: (x @ w).to(torch.bfloat16))(*values(
+        Xq.view(torch.uint8)[t].view(F8), xs[t], Wq[e], ws[e])) for e in range(len(counts))
+        if (t := tok[off[e]:off[e + 1]].long()).numel()])
+    need = q.qg_workspace_size(q.QG_OP_GEMM_FP8_EXPERTS, tok.numel(), 11008, 528)
+    for fill in (0, 0xFF, 0x5A):
+        ws8 = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        for _ in range(2):
+            assert torch.equal(experts(Xq, xs, tok, off, Wq, ws, tok.numel(), workspace=ws8), want)
+    assert q.qg_device_status() == q.QG_OK
+
+
 def test_experts_two_graphs():
-    sets = [expert_operands(16, 12, 1024, 1040, c, 30) for c in ([1, 0, 4] * 4, [40, 3, 0, 21] * 3)]
+    sets = [expert_operands(16, 12, 8192, 1040, c, 30) for c in ([1, 0, 4] * 4, [40, 3, 0, 21] * 3)]
     want = [experts(*o, o[2].numel()) for o in sets]
     graphs, outs = [], []
     for o in sets:
