@@ -13,7 +13,7 @@
 // the MMA's MN-major operand.  A dense product is the experts' product with one expert that has
 // all the rows.
 //
-// Every wait is bounded (mbar_wait); one that gives up records QG_ERR_TIMEOUT, and the role
+// Every wait is bounded (2 s); one that gives up records QG_ERR_TIMEOUT, and the role
 // stops issuing, waits for its own copies and MMAs, and leaves.
 #pragma once
 #include <type_traits>
@@ -30,6 +30,7 @@ struct Fp8Params {
     const int32_t* offsets;  // [E + 1], or NULL: one expert with all S slots
     uint16_t* Y;             // [S][N]
     int Mx, S, E, K, N, G, NB;
+    int join_rows;           // rows of a tile, about
     int box;                 // rows of a TMA box of activations: what a tile can have
     bool bf16;
     // the workspace of split tiles
@@ -62,14 +63,29 @@ QG_DEV_INLINE void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.
 template <int R>
 QG_DEV_INLINE void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// A bounded wait like mbar_wait's that looks at the clock and the limit only after many polls:
-// here a wait is mostly a few hundred cycles long and lies on the chain between the tensor core
-// and the warps that fold.
+// A bounded wait in a few instructions: 2 million polls of at most 1 us each, then QG_ERR_TIMEOUT
+// and false.  The waits lie between the steps of loops whose instructions have to stay at hand:
+// with mbar_wait's clock and limit inlined in each, a product of 8192 x 8192 x 28672 took 4 % longer.
 QG_DEV_INLINE bool short_wait(uint64_t* bar, uint32_t parity)
 {
-    for (uint32_t it = 0; it < 256; ++it)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait(bar, parity);
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        ".reg .u32 n;\n\t"
+        "mov.u32 n, 2000000;\n\t"
+        "POLL:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 p, n, 0;\n\t"
+        "@p bra POLL;\n\t"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (!ok) set_status(7u);
+    return ok != 0;
 }
 
 // One lane of the (converged) warp.  The role loops below run warp-uniform and only the TMA,
@@ -205,9 +221,9 @@ QG_DEV_INLINE void fp8_fold(float (&acc)[CW], uint32_t addr, float sc, F release
 // it, so a replayed graph finds it so again.
 // ---------------------------------------------------------------------------
 // Splitting costs the join: about 11 us for a few rows and 20 us for 128, where a step of 128
-// columns takes 0.32 us, so the longest CTA has to save fp8_min_saved() steps.  K = 11008, N =
-// 4096, 4 rows (86 steps down to 19): 27.5 -> 17.1 us; K = 4096 (32 down to 7): 11.8 -> 13.8 us,
-// left whole; K = 11008 with 128 rows: no difference.
+// columns takes 0.32 us (256: 0.6), so the longest CTA has to save fp8_min_saved() steps of 128
+// columns.  K = 11008, N = 4096, 4 rows (86 steps down to 19): 27.5 -> 17.1 us; K = 4096 (32 down
+// to 7): 11.8 -> 13.8 us, left whole; K = 11008 with 128 rows: no difference.
 constexpr int kFp8MinUnits = 4;   // of a piece
 __host__ __device__ inline int fp8_min_saved(int rows) { return 34 + rows / 4; }
 
@@ -219,7 +235,8 @@ struct Fp8Work {   // in shared memory: the folding threads have no registers to
     int64_t units;   // of all split tiles
     int64_t u0;      // this CTA's: [u0, u0 + n)
     int n;
-    QG_DEV_INLINE void init(int tiles, int rows, int G_, int grid_, int cta_)
+    // `wide`: columns of a tile over 128; `rows`: of a tile, about
+    QG_DEV_INLINE void init(int tiles, int wide, int rows, int G_, int grid_, int cta_)
     {
         G = G_;
         grid = grid_;
@@ -229,7 +246,7 @@ struct Fp8Work {   // in shared memory: the folding threads have no registers to
         units = u0 = 0;
         const int left = tiles % grid;
         const int parts = left ? (int)min((int64_t)grid, max((int64_t)left, (int64_t)left * G / kFp8MinUnits)) : 1;
-        if (G - (int)((int64_t)left * G / parts) >= fp8_min_saved(rows) && left > 0) {
+        if (left > 0 && (G - (int)((int64_t)left * G / parts)) * wide >= fp8_min_saved(rows)) {
             whole = tiles / grid;
             base = tiles - left;
             units = (int64_t)left * G;
@@ -419,7 +436,7 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
     // the experts' offsets come from the kernel before; a dense product's schedule does not
     if (p.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!fp8_schedule<C::BM>(sched, p, slabs)) return;
-    if (threadIdx.x == 0) work.init(sched.pre[p.E], p.box, G, gridDim.x, blockIdx.x);
+    if (threadIdx.x == 0) work.init(sched.pre[p.E], BN / 128, p.join_rows, G, gridDim.x, blockIdx.x);
     __syncthreads();
     if (work.steps() == 0) return;
     if (warp == 1) {

@@ -46,7 +46,7 @@ struct Fp8Workspace {
 Fp8Workspace fp8_carve(int S, int K, bool experts)
 {
     const size_t grid = num_sms();
-    const bool split = (K + 127) / 128 > qg::fp8_min_saved(fp8_box(S));
+    const bool split = (K + 127) / 128 * 2 > qg::fp8_min_saved(experts ? 1 : fp8_box(S));
     Fp8Workspace w;
     w.partials = (grid * 8 + 255) / 256 * 256;
     w.rows = split ? w.partials + grid * 2 * 128 * 256 * sizeof(float) : 0;
@@ -135,6 +135,8 @@ qg_status fp8_gemm(const uint8_t* Xq, const float* xs, int Mx, int K, const int3
     p.G = (K + 127) / 128;
     p.NB = (N + 127) / 128;
     p.bf16 = ydt == QG_BF16;
+    // an expert's tiles have some four times the average of rows at most, mostly
+    p.join_rows = offsets ? (int)std::min<int64_t>(fp8_box(S), 4 * (((int64_t)S + E - 1) / E)) : fp8_box(S);
     p.box = fp8_box(S);   // the rest of a tile holds what it held: rows of sums that go nowhere
     // 256 columns a tile where those tiles still fill half of the GPU
     const int64_t m_tiles = (int64_t)(S + 127) / 128 + (offsets ? std::min(S, E) / 2 : 0);
