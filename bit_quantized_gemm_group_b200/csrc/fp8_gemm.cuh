@@ -333,8 +333,12 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const Fp8Params p, const 
 // 4..11 fold: thread = row, BN / 2 columns, whose weight scale is one number, so a step costs a
 // thread one scale (which it loads itself, four groups ahead) and BN / 2 fma.
 //
-// Few rows: the tensor core then multiplies mostly zeros, but a step's weights (16 or 32 KB)
-// take HBM as long as a step takes the tensor core.  Mapped rows are gathered by
+// Measured: 8192 x 8192 x 28672 2.0 ms (1.9 PFLOP/s; the fold bounds it, and the power cap);
+// 4096 x 4096 x 4096 78 us; 1 x 4096 x 12288 13.3 us (3.8 TB/s), 16 x 8192 x 28672 42 us
+// (5.6 TB/s).
+// Few rows: the tensor core then multiplies rows that go nowhere, but a step's weights (16 or
+// 32 KB) take HBM as long as a step takes the tensor core; with operands swapped and a narrow N
+// it was no faster.  Mapped rows are gathered by
 // fp8_rows_kernel before it (TMA's gather of four rows an instruction took three times as long
 // as a step's MMAs).
 // ---------------------------------------------------------------------------
@@ -565,7 +569,9 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
         int b = 0;
         uint32_t bp = 0;
         open();
-        for (int i = 0; more && ok; ++i) {
+        // after a wait that gave up, the pieces of split tiles are still counted in, without work: a
+        // replay of this launch starts from cleared counters
+        for (int i = 0; more; ++i) {
             float acc[HW];
 #pragma unroll
             for (int t = 0; t < HW; ++t) acc[t] = 0.0f;

@@ -360,6 +360,7 @@ COUNTS = {
     "even": [40] * 12,
     "many": [3] * 100,
     "large": [700, 0, 513, 300],
+    "512 experts": [0] * 200 + [2, 0, 130] + [0] * 308 + [1],
 }
 
 
@@ -456,6 +457,30 @@ def test_experts_two_graphs():
         torch.cuda.synchronize()
         for Y, w in zip(outs, want):
             assert torch.equal(Y.view(torch.int16), w.view(torch.int16))
+
+
+def test_gemm_outputs_past_32_bits():
+    """More than 2^31 outputs."""
+    M, K, N = 75008, 16, 28688
+    o = exact_operands(M, K, N, 1)
+    Y = product(*o)
+    for rows in (slice(0, 3), slice(M - 3, M), slice(M // 2, M // 2 + 3)):
+        x, w = values(o[0][rows], o[1][rows], *o[2:])
+        assert torch.equal(Y[rows], (x @ w).to(torch.bfloat16))
+
+
+def test_experts_weights_past_32_bits():
+    """More than 2^31 weights: the last expert's lie behind them."""
+    E, K, N = 9, 16384, 16400
+    Xq, xs, Wl, wsl = exact_operands(5, K, N, 2)
+    Wq = torch.zeros(E, K, N, dtype=torch.uint8, device="cuda")
+    Wq[-1] = Wl.view(torch.uint8)
+    ws = torch.ones(E, cdiv(K, 128), cdiv(N, 128), device="cuda")
+    ws[-1] = wsl
+    off = torch.tensor([0] + [2] * (E - 1) + [5], dtype=torch.int32, device="cuda")
+    Y = experts(Xq, xs, None, off, Wq.view(F8), ws, 5)
+    x, w = values(Xq, xs, Wl, wsl)
+    assert not Y[:2].any() and torch.equal(Y[2:], (x @ w)[2:].to(torch.bfloat16))
 
 
 def test_empty():

@@ -264,7 +264,58 @@ def test_combine_bad_slots():
     assert torch.equal(Y[:, 0].float(), torch.tensor([0.5, 0.5, 0.0], device="cuda"))
 
 
+def test_combine_past_32_bits():
+    """More than 2^31 elements of slots: the last rows lie behind them."""
+    S, N = 270000, 8192
+    D = torch.zeros(S, N, dtype=torch.bfloat16, device="cuda")
+    D[-2:] = torch.randn(2, N, generator=gen(1), device="cuda").to(torch.bfloat16)
+    ts = torch.tensor([[S - 1, S - 2], [S - 2, -1]], dtype=torch.int32, device="cuda")
+    Y = torch.empty(2, N, dtype=torch.bfloat16, device="cuda")
+    q.qg_combine_experts(D, ts, torch.ones(2, 2, device="cuda"), Y)
+    assert torch.equal(Y[0], (D[-1].float() + D[-2].float()).to(torch.bfloat16)) and torch.equal(Y[1], D[-2])
+
+
 # ------------------------------------------------------------------------- a run of them
+def test_padded_tokens_go_nowhere():
+    """Tokens whose logits are -inf, and one that leaves two experts of four choices, through the whole layer."""
+    M, E, k, K, N = 20, 6, 4, 256, 128
+    g = gen(4)
+    X = torch.randn(M, K, generator=g, device="cuda").to(torch.bfloat16)
+    X[15:] = NAN                                     # padding holds anything
+    logits = torch.randn(M, E, generator=g, device="cuda")
+    logits[15:] = -INF
+    logits[3, 2:] = -INF
+    Wq = torch.randint(-3, 4, (E, K, N), generator=g, device="cuda").float().to(torch.float8_e4m3fn)
+    ws = torch.ones(E, 2, 1, device="cuda")
+    Xq, xs = torch.empty(M, K, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(M, 2, device="cuda")
+    idx, w = torch.empty(M, k, dtype=torch.int32, device="cuda"), torch.empty(M, k, device="cuda")
+    off, st = torch.empty(E + 1, dtype=torch.int32, device="cuda"), torch.empty(M * k, dtype=torch.int32, device="cuda")
+    ts, D = torch.empty_like(idx), torch.full((M * k, N), NAN, dtype=torch.bfloat16, device="cuda")
+    Y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    q.qg_quantize_act_fp8(X, Xq, xs)
+    assert q.qg_device_status() == q.QG_ERR_NONFINITE   # the padding
+    q.qg_route_topk(logits, None, idx, w)
+    q.qg_expert_slots(idx, off, st, ts)
+    q.qg_gemm_fp8_experts(Xq, xs, st, off, Wq, ws, D)
+    q.qg_combine_experts(D, ts, w, Y)
+    assert q.qg_device_status() == q.QG_OK
+    used = 15 * k - 2
+    assert int(off[-1]) == used and (st[used:] == -1).all() and (st[:used] >= 0).all()
+    assert torch.isnan(D[used:]).all() and not torch.isnan(D[:used]).any()
+    assert (ts[15:] == -1).all() and (ts[3, 2:] == -1).all()
+    assert not Y[15:].any() and not torch.isnan(Y).any()
+    y = torch.zeros(15, N, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(y)
+    for m in range(15):
+        x = Xq[m].double() * xs[m].double().repeat_interleave(128)
+        for e, v in zip(idx[m].tolist(), w[m].double().tolist()):
+            if e >= 0:
+                y[m] += v * (x @ Wq[e].double())
+                size[m] += v * (x.abs() @ Wq[e].double().abs())
+    # two roundings to bf16, 2^-8 each, and fp32 sums of 256 products: 2^-24 each
+    assert ((Y[:15].double() - y).abs() <= (2.0 ** -7 + 2.0 ** -15) * size).all()
+
+
 @pytest.mark.parametrize("captured", [False, True])
 @pytest.mark.parametrize("M,E,k,K,N", [(1, 16, 4, 512, 272), (50, 8, 2, 400, 528), (700, 16, 4, 512, 512)])
 def test_mixture_of_experts_layer(M, E, k, K, N, captured):
