@@ -163,7 +163,9 @@ QG_DEV_INLINE float unordered(uint32_t u) { return __uint_as_float(u ^ ((u >> 31
 // -- two keys, or the last group kept and the first dropped, nearer than the keys' error;
 // logits that binary64 scores cannot tell apart (saturated, or nearer than 2^-40) -- the token
 // is done again by route_exact: about one in two hundred of 256 experts with a bias.
-// Bound by the choice: 8 + 1 rounds of a maximum over the warp (16384 x 256, bias and groups).
+// Bound by the choice: 8 + 1 dependent rounds of a maximum over the warp (16384 x 256, top 8: 23 us
+// plain softmax, 46 us with bias and groups, of which 11 us for the second looks; the logits
+// alone take 1.3 us of HBM).
 template <int T, int VPL>
 __global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
 {
@@ -310,7 +312,9 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
 // choices, 128 for each warp in four rounds: in a round the lanes of equal choices find one
 // another (match), so a choice's rank is the warp's count so far plus the lanes before it;
 // then the warps' counts are summed up, and the blocks' (slot_count_kernel's, unless there is
-// but one).  Latency-bound: a launch and a handful of dependent steps each.
+// but one).  Latency-bound: a launch and a handful of dependent steps each (16 x 8 choices of 64
+// experts 4 us, 131072 of 256 experts 14 us; a scan of the block's choices by each thread and a
+// serial sum over the experts took 30 us).
 // ---------------------------------------------------------------------------
 constexpr int kSlotBlock = 4096, kSlotWarps = 32;
 
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(32 * kSlotWarps) slot_place_kernel(const SlotP
 }
 
 // Y[m] = rn( sum_j weights[m][j] D[token_slot[m][j]] ), j in order, fp32.  One thread per 8
-// columns of a token.  HBM-bound: every slot's row is read once.
+// columns of a token.  HBM-bound: every slot's row is read once (16384 x 8 x 4096: 207 us, 5.8 TB/s).
 template <bool BF16>
 __global__ void __launch_bounds__(256) combine_experts_kernel(const uint16_t* __restrict__ D, int S, int N, int M,
                                                               int topk, const int32_t* __restrict__ token_slot,
