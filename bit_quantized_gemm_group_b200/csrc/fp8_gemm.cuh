@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const Fp8Params p, const 
 // thread one scale (which it loads itself, four groups ahead) and BN / 2 fma.
 //
 // Measured: 8192 x 8192 x 28672 2.0 ms (1.9 PFLOP/s; the fold bounds it, and the power cap);
-// 4096 x 4096 x 4096 78 us; 1 x 4096 x 12288 13.3 us (3.8 TB/s), 16 x 8192 x 28672 42 us
+// 4096 x 4096 x 4096 78..93 us; 1 x 4096 x 12288 13.3 us (3.8 TB/s), 16 x 8192 x 28672 42 us
 // (5.6 TB/s).
 // Few rows: the tensor core then multiplies rows that go nowhere, but a step's weights (16 or
 // 32 KB) take HBM as long as a step takes the tensor core; with operands swapped and a narrow N
