@@ -326,8 +326,8 @@ def qg_awq_search(Xcal, W, n_grid, mse, best, s, inv_s, group=128, workspace="au
 # ---------------------------------------------------------------------------
 # The FP8 layer and its experts.  These calls check types and shapes here (a wrong
 # shape would read past a buffer), run on the device of their tensors and, with
-# workspace="auto", take their scratch from torch's allocator for the one call: calls on
-# several streams and captured graphs then share none.
+# workspace="auto", take their scratch from torch's allocator for the one call, from the pool
+# of the stream that the call runs on: calls on several streams and captured graphs share none.
 # ---------------------------------------------------------------------------
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 _HALF = {torch.float16: QG_F16, torch.bfloat16: QG_BF16}
@@ -352,6 +352,15 @@ def _rank(where, name, t, n):
         raise ValueError(f"{where}: {name} has {t.dim()} dimensions, not {n}")
 
 
+def _scratch(need, device, stream):
+    """`need` bytes of the pool of the stream that the call runs on.  A block of another stream's pool may
+    still be in use there: its order with this stream's work is only kept when the block is given back."""
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=device)
+
+
 def _run(where, device, stream, args, op=None, workspace=None):
     """Calls `where` with `args`, then (op = (op, M, K, N)) the workspace, then the stream, on GPU `device`."""
     if device != torch.cuda.current_device():
@@ -361,9 +370,7 @@ def _run(where, device, stream, args, op=None, workspace=None):
     if op is not None:
         if isinstance(workspace, str) and workspace == "auto":
             need = _lib.qg_workspace_size(*op)
-            workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-            if workspace is not None and stream is not None:
-                workspace.record_stream(stream)
+            workspace = _scratch(need, device, stream) if need else None
         if workspace is None or workspace is False:
             args += (None, 0)
         else:
