@@ -437,11 +437,14 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
         tma_prefetch_desc(&tm_w);
         tma_prefetch_desc(&tm_x);
     }
-    // the experts' offsets come from the kernel before; a dense product's schedule does not
+    // Whatever memory this kernel reads, weights and scales too, may have been written by the kernel
+    // before it, so every thread waits for that one first (and no bounded wait below counts the
+    // time of another kernel).  Only a dense product's schedule comes from the parameters alone.
     if (p.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!fp8_schedule<C::BM>(sched, p, slabs)) return;
     if (threadIdx.x == 0) work.init(sched.pre[p.E], BN / 128, p.join_rows, G, gridDim.x, blockIdx.x);
     __syncthreads();
+    if (!p.offsets) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (work.steps() == 0) return;
     if (warp == 1) {
         tmem_alloc(tslot, C::TMEM_COLS);
@@ -458,24 +461,8 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
             // ---------------- producer ----------------
             Fp8Walk<C::BM> walk(sched, p.E, slabs);
             const bool one = elect_one();
-            auto weights = [&](int s, int n0, int kb) {
-                uint8_t* st = smem + s * C::STAGE;
-                mbar_arrive_expect_tx(&full[s], C::B_BYTES + p.box * 128);
-                tma_load_3d(&tm_w, &full[s], st + C::A_BYTES, n0, kb * 128, walk.e);
-                if (BN == 256) tma_load_3d(&tm_w, &full[s], st + C::A_BYTES + 16384, n0 + 128, kb * 128, walk.e);
-            };
-            // weights do not depend on the kernel before: a dense product's first stages of them
-            // are requested before waiting for it
-            int early = 0, tile, k0, k1;
-            if (!p.offsets) {
-                for (int i = 0; early < ST && work.piece(i, tile, k0, k1); ++i) {
-                    walk.at(tile);
-                    for (int kb = k0; kb < k1 && early < ST; ++kb, ++early)
-                        if (one) weights(early, walk.slab * BN, kb);
-                }
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-            }
             bool ok = true;
+            int tile, k0, k1;
             int64_t issued = 0;
             int s = 0;
             uint32_t sp = 1;   // parity
@@ -483,13 +470,14 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
                 walk.at(tile);
                 const int s0 = walk.first(), n0 = walk.slab * BN;
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (issued >= early) {
-                        ok = all_wait(&empty[s], sp);
-                        if (!ok) break;
-                    }
+                    ok = all_wait(&empty[s], sp);
+                    if (!ok) break;
                     if (one) {
-                        if (issued >= early) weights(s, n0, kb);
-                        tma_load_2d(&tm_x, &full[s], smem + s * C::STAGE, kb * 128, s0);
+                        uint8_t* st = smem + s * C::STAGE;
+                        mbar_arrive_expect_tx(&full[s], C::B_BYTES + p.box * 128);
+                        tma_load_3d(&tm_w, &full[s], st + C::A_BYTES, n0, kb * 128, walk.e);
+                        if (BN == 256) tma_load_3d(&tm_w, &full[s], st + C::A_BYTES + 16384, n0 + 128, kb * 128, walk.e);
+                        tma_load_2d(&tm_x, &full[s], st, kb * 128, s0);
                     }
                     __syncwarp();
                     if (++s == ST) { s = 0; sp ^= 1; }
@@ -564,7 +552,6 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
             wp = p.ws + (int64_t)walk.e * G * p.NB + min(n0 / 128, p.NB - 1);
             load(k0 & ~3);
         };
-        asm volatile("griddepcontrol.wait;" ::: "memory");   // xs, Y and the workspace follow the kernel before
         bool ok = true, more = work.piece(0, tile, k0, k1);
         int b = 0;
         uint32_t bp = 0;

@@ -471,6 +471,8 @@ qg_status qg_quantize_weight_fp8(const void* W, qg_dtype wdt, int E, int K, int 
  * Xq e4m3 [M][K], xs fp32 [M][G], Wq e4m3 [K][N], ws fp32 [G][NB] as above; any fp32
  * scales are taken, not only the quantizers'.  Y fp16 or bf16 [M][N] (ydt).
  * NaN codes and scales give NaN in the rows and columns that read them, and there only.
+ * Everything the call reads, weights and scales among it, may be written by the kernel right
+ *   before it in the same stream, whether that lets its dependents start early or not.
  * Rules: K % 16 == 0, N % 16 == 0.
  * workspace: required when qg_workspace_size(QG_OP_GEMM_FP8, M, K, N) is not 0, and then
  *   at least that many bytes (NULL -> QG_ERR_NULL, smaller -> QG_ERR_WORKSPACE); contents

@@ -206,3 +206,71 @@ def test_captured_on_two_streams(kind, a, b):
         eager.call(stream=third)
         check(turn, here, there, eager)
     assert q.qg_device_status() == q.QG_OK
+
+
+# ------------------------------------------------- operands that the kernel right before has written (GPU)
+@pytest.mark.gpu
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_weights_quantized_right_before(M, captured):
+    """A served layer whose weight is updated: the weight quantizer is the last kernel before the product."""
+    K, N = 2048, 1040
+    Xq, xs = operands(M, K, N, 1, 5)[:2]
+    W = torch.zeros(K, N, device="cuda")
+    Wq, ws = torch.empty(K, N, dtype=F8, device="cuda"), torch.empty(K // 128, -(-N // 128), device="cuda")
+    Y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+
+    def update():
+        q.qg_quantize_weight_fp8(W, Wq, ws)
+        q.qg_gemm_fp8(Xq, xs, Wq, ws, Y)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            update()
+    g = torch.Generator(device="cuda").manual_seed(M)
+    for turn in range(20):
+        # codes -448 and 448 under the scale 1 (and the powers of two beside it): every sum is exact
+        W.copy_((torch.randint(0, 2, (K, N), generator=g, device="cuda").float() * 2 - 1) * 448 * 2.0 ** (turn % 3))
+        Y.fill_(NAN)
+        torch.cuda.synchronize()
+        graph.replay() if captured else update()
+        want = value(Xq, xs, False) @ W.double()
+        assert torch.equal(Y, want.to(torch.bfloat16)), turn
+    assert q.qg_device_status() == q.QG_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("captured", [False, True])
+def test_weights_written_by_a_kernel_that_lets_the_product_start_early(captured):
+    """The bytes of one product's outputs are the next one's weights.  The first occupies some 32 SMs, so the second
+    starts beside it."""
+    K1, K2, N1 = 4096, 256, 2048
+    one = torch.ones(1, device="cuda")
+    eye = torch.eye(K2, K1, device="cuda").to(F8)             # Y1 = the first rows of the first weight
+    s1, t1 = one.expand(K2, K1 // 128).contiguous(), one.expand(K1 // 128, N1 // 128).contiguous()
+    X2, s2 = operands(7, K2, 16, 1, 6)[:2]
+    t2 = one.expand(K2 // 128, 2 * N1 // 128).contiguous()
+    W1 = torch.empty(K1, N1, dtype=F8, device="cuda")
+    Y1 = torch.empty(K2, N1, dtype=torch.bfloat16, device="cuda")
+    W2 = Y1.view(torch.uint8).view(F8)                        # of 1.0 and 2.0: the codes -0, 1.875, 0 and 2
+    Y2 = torch.empty(7, 2 * N1, dtype=torch.bfloat16, device="cuda")
+
+    def both():
+        q.qg_gemm_fp8(eye, s1, W1, t1, Y1)
+        q.qg_gemm_fp8(X2, s2, W2, t2, Y2)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            both()
+    g = torch.Generator(device="cuda").manual_seed(8)
+    for turn in range(20):
+        W1.copy_(torch.randint(1, 3, (K1, N1), generator=g, device="cuda").float())
+        Y1.zero_()
+        torch.cuda.synchronize()
+        graph.replay() if captured else both()
+        torch.cuda.synchronize()
+        assert torch.equal(Y1.float(), W1[:K2].float())
+        assert torch.equal(Y2, (value(X2, s2, False) @ W2.double()).to(torch.bfloat16)), turn
+    assert q.qg_device_status() == q.QG_OK
