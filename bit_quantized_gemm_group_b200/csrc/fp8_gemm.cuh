@@ -176,11 +176,13 @@ struct Fp8Walk {
     QG_DEV_INLINE int rows() const { return min(T, sc.off[e + 1] - first()); }
 };
 
-// The row of Xq that slot s reads; -1 where the map is wrong.
+// The row of Xq that slot s reads; -1 where the map is wrong.  Maps, scales and rows are read with
+// plain loads: a kernel that this one started beside may write them until the wait for it, and the
+// read-only path (__ldg) is for memory that nothing writes during the whole launch.
 QG_DEV_INLINE int fp8_row(const Fp8Params& p, int s)
 {
     if (!p.rows) return s;
-    const int r = __ldg(p.rows + s);
+    const int r = p.rows[s];
     return (uint32_t)r < (uint32_t)p.Mx ? r : -1;
 }
 
@@ -309,8 +311,7 @@ QG_DEV_INLINE bool fp8_arrive(unsigned long long* word, unsigned long long token
 // The mapped rows in slot order, for the tile kernel (a wrong map entry: row 0, whose sums go
 // nowhere).  Four slots and 4 KB of K per CTA, 64 threads a slot.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) fp8_rows_kernel(const Fp8Params p, const uint8_t* __restrict__ Xq,
-                                                       uint8_t* __restrict__ xg)
+__global__ void __launch_bounds__(256) fp8_rows_kernel(const Fp8Params p, const uint8_t* Xq, uint8_t* xg)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -318,12 +319,14 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const Fp8Params p, const 
     if (s >= min(p.offsets[p.E], p.S)) return;
     const uint4* src = reinterpret_cast<const uint4*>(Xq + (int64_t)max(fp8_row(p, s), 0) * p.K);
     uint4* dst = reinterpret_cast<uint4*>(xg + (int64_t)s * p.K);
-    const int end = min(p.K / 16, ((int)blockIdx.y + 1) * 256);
+    const int k0 = blockIdx.y * 256 + (threadIdx.x & 63), end = min(p.K / 16, ((int)blockIdx.y + 1) * 256);
+    uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int k = blockIdx.y * 256 + i * 64 + (threadIdx.x & 63);
-        if (k < end) dst[k] = __ldg(src + k);
-    }
+    for (int i = 0; i < 4; ++i)
+        if (k0 + 64 * i < end) v[i] = src[k0 + 64 * i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (k0 + 64 * i < end) dst[k0 + 64 * i] = v[i];
 }
 
 // ---------------------------------------------------------------------------
@@ -531,14 +534,14 @@ __global__ void __launch_bounds__(Fp8TileCfg<BN>::THREADS, 1)
         const float *xp, *wp;
         auto load = [&](int kb) {
             if (vec) {
-                const float4 v = __ldg(reinterpret_cast<const float4*>(xp + kb));
+                const float4 v = *reinterpret_cast<const float4*>(xp + kb);
                 x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = __ldg(xp + min(kb + j, G - 1));
+                for (int j = 0; j < 4; ++j) x[j] = xp[min(kb + j, G - 1)];
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = __ldg(wp + (int64_t)min(kb + j, G - 1) * p.NB);
+            for (int j = 0; j < 4; ++j) w[j] = wp[(int64_t)min(kb + j, G - 1) * p.NB];
         };
         auto open = [&]() {
             Fp8Walk<C::BM> walk(sched, p.E, slabs);

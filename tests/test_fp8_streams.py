@@ -274,3 +274,39 @@ def test_weights_written_by_a_kernel_that_lets_the_product_start_early(captured)
         assert torch.equal(Y1.float(), W1[:K2].float())
         assert torch.equal(Y2, (value(X2, s2, False) @ W2.double()).to(torch.bfloat16)), turn
     assert q.qg_device_status() == q.QG_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("M,K,N", [(5, 1024, 528), (200, 1024, 528), (12, 11008, 272)])
+def test_maps_written_right_before_in_buffers_that_are_still_being_read(M, K, N, captured):
+    """Layer after layer with the same map buffers: each product starts beside the one before, which reads the old maps."""
+    E, k, layers = 16, 4, 6
+    Xq, xs, Wq, ws = operands(M, K, N, E, M)
+    g = torch.Generator(device="cuda").manual_seed(M + 1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    idx = [torch.zeros(M, k, **i32) for _ in range(layers)]
+    off, token, slot = torch.empty(E + 1, **i32), torch.empty(M * k, **i32), torch.empty(M, k, **i32)
+    Y = [torch.empty(M * k, N, dtype=torch.bfloat16, device="cuda") for _ in range(layers)]
+
+    def run():
+        for i, y in zip(idx, Y):
+            q.qg_expert_slots(i, off, token, slot)
+            q.qg_gemm_fp8_experts(Xq, xs, token, off, Wq, ws, y)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+    every = torch.einsum("mk,ekn->emn", value(Xq, xs, False), value(Wq, ws, True)).to(torch.bfloat16)
+    for turn in range(8):
+        for i, y in zip(idx, Y):
+            i.copy_(torch.rand(M, E, generator=g, device="cuda").topk(k, 1).indices)
+            y.fill_(NAN)
+        torch.cuda.synchronize()
+        graph.replay() if captured else run()
+        torch.cuda.synchronize()
+        for i, y in zip(idx, Y):
+            order = i.flatten().long().sort(stable=True)
+            assert torch.equal(y, every[order.values, order.indices // k]), turn
+    assert q.qg_device_status() == q.QG_OK
