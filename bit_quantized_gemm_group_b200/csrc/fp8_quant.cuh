@@ -48,11 +48,12 @@ struct Fp8Scale {
     // numbers, and the code only where that midpoint is next to a midpoint c (5 significant
     // bits) of two e4m3 numbers.  x - c s is then a multiple of s's last bit times 2^-4, which
     // forces s to within two last bits of a multiple of 1/8 and x = c k / 8, and then x / s is
-    // off that fp32 midpoint by more than the bound.  Three instructions for about ten.
+    // off that fp32 midpoint by more than the bound.  The remainder is taken as q0 s - x, whose zero is
+    // +0 for x of either sign, so that -0 stays -0 as in the quotient.  Three instructions for about ten.
     QG_DEV_INLINE float quick(float x) const
     {
         const float q0 = __fmul_rn(x, r);
-        return fmaf(fmaf(-q0, s, x), r, q0);
+        return fmaf(-fmaf(q0, s, -x), r, q0);
     }
 };
 
