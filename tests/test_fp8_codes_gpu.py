@@ -56,3 +56,22 @@ def test_weights_keep_the_sign_of_zero(dtype):
         q.qg_quantize_weight_fp8(W, Wq, ws)
         assert torch.equal(Wq.view(torch.uint8), bytes_of(W, W.float().abs().amax().expand(128, 128)))
     assert q.qg_device_status() == q.QG_OK
+
+
+def test_every_fp16_quotient():
+    """Every fp16 significand under the scale of every other one, over 21 binades: from the largest code to zero."""
+    sig = torch.arange(1024, 2048, device="cuda") / 1024.0
+    amax = sig * 2.0 ** 15                           # a row each; the largest is 65504
+    part = torch.cat([sig, sig[:119]]).view(9, 127)  # nine groups of 127 beside the largest
+    x = part[None] * torch.exp2(15.0 - torch.arange(21, device="cuda"))[:, None, None]       # [21, 9, 127]
+    x = torch.minimum(x.reshape(1, 189, 127), amax[:, None, None])
+    x[..., ::2] *= -1.0
+    X = torch.cat([amax[:, None, None].expand(1024, 189, 1), x], 2).to(torch.float16).view(1024, 189 * 128)
+    assert torch.equal(X.view(1024, 189, 128)[..., 1:].float(), x)      # all of them are fp16 numbers
+    Xq, xs = torch.empty(X.shape, dtype=F8, device="cuda"), torch.empty(1024, 189, device="cuda")
+    q.qg_quantize_act_fp8(X, Xq, xs)
+    for rows in range(0, 1024, 128):
+        at = slice(rows, rows + 128)
+        want = bytes_of(X[at], amax[at, None].expand(128, 189 * 128))
+        assert torch.equal(Xq[at].view(torch.uint8), want)
+    assert q.qg_device_status() == q.QG_OK
