@@ -163,7 +163,8 @@ QG_DEV_INLINE float unordered(uint32_t u) { return __uint_as_float(u ^ ((u >> 31
 // -- two keys, or the last group kept and the first dropped, nearer than the keys' error;
 // logits that binary64 scores cannot tell apart (saturated, or nearer than 2^-40) -- the token
 // is done again by route_exact: about one in two hundred of 256 experts with a bias.
-// Bound by the choice: 8 + 1 dependent rounds of a maximum over the warp (16384 x 256, top 8: 23 us
+// The weights of the chosen are binary64 values, one lane each, rounded once (0.2 to 1 us of the times below).
+// Bound by the choice: 8 + 1 dependent rounds of a maximum over the warp (16384 x 256, top 8: 25 us
 // plain softmax, 46 us with bias and groups, of which 11 us for the second looks; the logits
 // alone take 1.3 us of HBM).
 template <int T, int VPL>
@@ -200,10 +201,10 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
         return;
     }
     // fp32 scores, where they are needed: each is within 2^-20 of its value
-    double sum = 0.0;
     const bool scores = p.bias || p.n_group > 1;
-    if (scores || (!p.sigmoid && !p.renorm)) {
+    if (scores) {
         float sc[VPL];
+        double sum = 0.0;
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
             sc[v] = p.sigmoid ? __frcp_rn(1.0f + expf(-x[v])) : mx > -kInf ? expf(x[v] - mx) : 0.0f;
@@ -283,27 +284,24 @@ __global__ void __launch_bounds__(128) route_topk_kernel(const RouteParams p)
         route_exact<T, VPL>(p, mx, false, skey[warp], m, lane);
         return;
     }
-    float w = 0.0f;   // within 16 * 2^-24 of its value in all
-    if (ej >= 0) {
-        if (p.sigmoid) {
-            w = __frcp_rn(1.0f + expf(-xj));
-        } else {   // exp of the exact difference: d and what its rounding left out
-            const float d = xj - mx, t = d - xj, left = (xj - (d - t)) + (-mx - t);
-            w = expf(d);
-            w = fmaf(w, left, w);
-        }
-    }
+    // the weights in binary64, a lane each, rounded once
+    double w = 0.0;
+    if (ej >= 0) w = p.sigmoid ? 1.0 / (1.0 + exp(-(double)xj)) : exp((double)xj - (double)mx);
     if (p.renorm) {
-        float total = w;
+        double total = w;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        w = total > 0.0f ? __fdiv_rn(w, total) : 0.0f;
-    } else if (!p.sigmoid && ej >= 0) {
-        w = (float)((double)w / sum);
+        w = total > 0.0 ? w / total : 0.0;
+    } else if (!p.sigmoid && mx > -kInf) {   // by the sum over all experts
+        double sum = 0.0;
+        for (int e = lane; e < E; e += 32) sum += exp((double)load_logit<T>(p.logits, (int64_t)m * E + e) - (double)mx);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        w /= sum;
     }
     if (lane < p.topk) {
         p.idx[(int64_t)m * p.topk + lane] = ej;
-        p.weights[(int64_t)m * p.topk + lane] = w * p.scale;
+        p.weights[(int64_t)m * p.topk + lane] = (float)(w * (double)p.scale);
     }
 }
 
