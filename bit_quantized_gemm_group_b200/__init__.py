@@ -34,7 +34,7 @@ EXPORTS = ["qg_quantize_w4_group", "qg_pack_nibbles", "qg_gemm_w4a16", "qg_smoot
            "qg_outlier_side_add", "qg_gemm_w4a16_outlier", "qg_prune24", "qg_pack24_vals", "qg_gemm_w4a16_24",
            "qg_gptq", "qg_gptq_blocked", "qg_pack24_tc", "qg_gemm_w4a16_24_tc", "qg_quantize_act_fp8",
            "qg_quantize_weight_fp8", "qg_gemm_fp8", "qg_route_topk", "qg_expert_slots", "qg_gemm_fp8_experts",
-           "qg_combine_experts"]
+           "qg_combine_experts", "qg_selftest_split_wait"]
 
 
 class QgError(RuntimeError):
@@ -80,6 +80,7 @@ _SIGS = {
     "qg_combine_experts": [_P, _I, _I, _I, _P, _P, _I, _I, _P, _P],
     "qg_device_status": [_P],
     "qg_selftest_bounded_wait": [ctypes.c_uint64, _P],
+    "qg_selftest_split_wait": [ctypes.c_uint32, _I, _P, _P, _P],
 }
 
 
@@ -496,6 +497,19 @@ def qg_device_status(stream=None) -> int:
 
 def qg_selftest_bounded_wait(limit_ns: int = 0, stream=None):
     _check(lib().qg_selftest_bounded_wait(limit_ns, _stream(stream)), "qg_selftest_bounded_wait")
+
+
+def qg_selftest_split_wait(polls, counter, result, stream=None):
+    """Waits that run out after `polls` polls in result.numel() blocks, which then count themselves in at `counter`
+    (int64 [1]) -> result int32 [pieces]: 1 where the wait gave up, plus 2 where the block was the last."""
+    f = "qg_selftest_split_wait"
+    _rank(f, "result", result, 1)
+    dev = result.get_device()
+    _want(f, "result", result, (torch.int32,), (result.shape[0],), dev)
+    _want(f, "counter", counter, (torch.int64,), (1,), dev)
+    if not 0 < polls < 1 << 32:
+        raise ValueError(f"{f}: polls is {polls}")
+    _run(f, dev, stream, (polls, result.shape[0], counter.data_ptr(), result.data_ptr()))
 
 
 def qg_status_string(status: int) -> str:

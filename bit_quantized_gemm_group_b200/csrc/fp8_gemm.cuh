@@ -63,16 +63,17 @@ QG_DEV_INLINE void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.
 template <int R>
 QG_DEV_INLINE void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// A bounded wait in a few instructions: 2 million polls of at most 1 us each, then QG_ERR_TIMEOUT
-// and false.  The waits lie between the steps of loops whose instructions have to stay at hand:
+// A bounded wait in a few instructions: kFp8Polls polls, then QG_ERR_TIMEOUT and false.  A poll that
+// finds nothing is suspended for 4.0 us (measured, with a hint of 1 us), so that all of them take 2 s.  The waits lie between the steps of loops whose instructions have to stay at hand:
 // with mbar_wait's clock and limit inlined in each, a product of 8192 x 8192 x 28672 took 4 % longer.
-QG_DEV_INLINE bool short_wait(uint64_t* bar, uint32_t parity)
+constexpr uint32_t kFp8Polls = 500000;
+QG_DEV_INLINE bool short_wait(uint64_t* bar, uint32_t parity, uint32_t polls = kFp8Polls)
 {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         ".reg .u32 n;\n\t"
-        "mov.u32 n, 2000000;\n\t"
+        "mov.u32 n, %3;\n\t"
         "POLL:\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
         "@p bra DONE;\n\t"
@@ -82,7 +83,7 @@ QG_DEV_INLINE bool short_wait(uint64_t* bar, uint32_t parity)
         "DONE:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(polls)
         : "memory");
     if (!ok) set_status(7u);
     return ok != 0;
@@ -106,9 +107,9 @@ QG_DEV_INLINE bool elect_one()
 QG_DEV_INLINE int uniform_warp() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
 
 // every lane waits; the result is the warp's
-QG_DEV_INLINE bool all_wait(uint64_t* bar, uint32_t parity)
+QG_DEV_INLINE bool all_wait(uint64_t* bar, uint32_t parity, uint32_t polls = kFp8Polls)
 {
-    return __all_sync(0xffffffffu, short_wait(bar, parity));
+    return __all_sync(0xffffffffu, short_wait(bar, parity, polls));
 }
 
 // ---------------------------------------------------------------------------
@@ -305,6 +306,21 @@ QG_DEV_INLINE bool fp8_arrive(unsigned long long* word, unsigned long long token
         if (seen == old) return last;
         old = seen;
     }
+}
+
+// Self-test: each block (a warp) is a piece of one split tile whose wait runs out, on a barrier
+// that nothing arrives at, and counts itself in without work.  result: 1 where the wait gave up,
+// plus 2 in the piece that arrived last.  No block waits for another.
+__global__ void fp8_selftest_wait_kernel(uint32_t polls, unsigned long long* word, unsigned long long token, int32_t* result)
+{
+    __shared__ __align__(8) uint64_t bar;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    const bool ok = all_wait(&bar, 0, polls);
+    if (threadIdx.x == 0) result[blockIdx.x] = (ok ? 0 : 1) + (fp8_arrive(word, token, gridDim.x) ? 2 : 0);
 }
 
 // ---------------------------------------------------------------------------

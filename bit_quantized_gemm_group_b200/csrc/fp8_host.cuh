@@ -73,6 +73,15 @@ qg_status fp8_check_registers(Kern kern)
     return QG_OK;
 }
 
+// A token for the counters of split tiles: its low byte is 0, the rest is not.
+unsigned long long fp8_token()
+{
+    unsigned long long t;
+    do t = next_decode_token() << 8;
+    while (t == 0);
+    return t;
+}
+
 // The weights as {N, K, E} (boxes of 128 columns x 128 k), the activations as {K, rows} (boxes of
 // 128 k x p.box rows).
 qg_status fp8_maps(CUtensorMap* tw, CUtensorMap* tx, const uint8_t* X, int rows, const uint8_t* Wq, const qg::Fp8Params& p)
@@ -97,8 +106,7 @@ qg_status launch_fp8_tile(qg::Fp8Params p, const uint8_t* X, const uint8_t* Wq, 
     uint8_t* base = static_cast<uint8_t*>(ws);
     p.counters = reinterpret_cast<unsigned long long*>(base);
     p.partials = reinterpret_cast<float*>(base + w.partials);
-    do p.token = next_decode_token() << 8;
-    while (p.token == 0);
+    p.token = fp8_token();
     int rows = p.Mx;
     if (p.rows) {
         const dim3 g((p.S + 3) / 4, (p.K + 4095) / 4096);

@@ -1633,6 +1633,17 @@ qg_status qg_selftest_bounded_wait(uint64_t limit_ns, qg_stream_t stream)
     return QG_OK;
 }
 
+qg_status qg_selftest_split_wait(uint32_t polls, int pieces, uint64_t* counter, int32_t* result, qg_stream_t stream)
+{
+    if (polls < 1 || polls > qg::kFp8Polls || pieces < 1 || pieces > 255) return QG_ERR_SHAPE;
+    if (!counter || !result) return QG_ERR_NULL;
+    if (misaligned(counter) || misaligned(result)) return QG_ERR_ALIGN;
+    qg::fp8_selftest_wait_kernel<<<pieces, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        polls, reinterpret_cast<unsigned long long*>(counter), fp8_token(), result);
+    QG_CUDA(cudaGetLastError());
+    return QG_OK;
+}
+
 }  // extern "C"
 
 // ===========================================================================

@@ -570,6 +570,15 @@ const char* qg_last_error(void);
  * device status then reads QG_ERR_TIMEOUT.  No fault, trap or hang is involved. */
 qg_status qg_selftest_bounded_wait(uint64_t limit_ns, qg_stream_t stream);
 
+/* The same for the FP8 product's waits and the count of a split tile's pieces: launches `pieces`
+ * (1 .. 255) blocks that each wait on a barrier nothing will complete, for `polls` polls (1 ..
+ * 500000, the product's own limit, some 2 s), and then count themselves in at `counter` (one
+ * word, any contents) without work, as the product does after such a wait.
+ * result[i] (int32 [pieces]): 1 where block i's wait gave up, plus 2 where it arrived last; the
+ * last one leaves the counter 0.  The device status then reads QG_ERR_TIMEOUT. */
+qg_status qg_selftest_split_wait(uint32_t polls, int pieces, uint64_t* counter, int32_t* result,
+                                 qg_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
