@@ -177,7 +177,7 @@ bool slots_bad_shape(int M, int topk, int E)
 size_t slots_workspace(int M, int topk, int E)
 {
     const size_t blocks = ((size_t)M * topk + qg::kSlotBlock - 1) / qg::kSlotBlock;
-    return blocks > 1 ? (blocks * E * sizeof(int32_t) + 255) / 256 * 256 : 0;
+    return blocks > 1 ? ((blocks + (blocks > qg::kSlotSum)) * E * sizeof(int32_t) + 255) / 256 * 256 : 0;
 }
 
 qg_status expert_slots(const int32_t* idx, int M, int topk, int E, int32_t* offsets, int32_t* slot_token,
@@ -196,6 +196,10 @@ qg_status expert_slots(const int32_t* idx, int M, int topk, int E, int32_t* offs
     const dim3 threads(32 * qg::kSlotWarps);
     if (blocks > 1) {
         const qg_status r = launch_pdl(qg::slot_count_kernel, dim3(blocks), threads, 0, stream, p);
+        if (r != QG_OK) return r;
+    }
+    if (blocks > qg::kSlotSum) {
+        const qg_status r = launch_pdl(qg::slot_sum_kernel, dim3((E + 31) / 32), dim3(1024), 0, stream, p);
         if (r != QG_OK) return r;
     }
     return launch_pdl(qg::slot_place_kernel, dim3(blocks), threads, 0, stream, p);
