@@ -9,7 +9,7 @@ namespace {
 template <int T>
 qg_status quantize_act_fp8(const void* X, int M, int K, uint8_t* Xq, float* xs, qg_stream_t stream)
 {
-    const uint32_t G = (K + 127) / 128;
+    const uint32_t G = ((uint32_t)K + 127) / 128;
     const uint64_t groups = (uint64_t)M * G;
     if (groups > 0xFFFFFF00ull) return QG_ERR_SHAPE;
     const uint32_t grid = (uint32_t)((groups + 31) / 32);
@@ -31,7 +31,12 @@ qg_status quantize_weight_fp8(const void* W, int E, int K, int N, uint8_t* Wq, f
 // ---------------------------------------------------------------------------
 // FP8 products
 // ---------------------------------------------------------------------------
-bool fp8_bad_shape(int K, int N) { return K < 16 || K % 16 || N < 16 || N % 16; }
+// Rows, K and N are rounded up to tiles of at most 256 in 32 bits.
+bool fp8_bad_shape(int M, int K, int N)
+{
+    constexpr int most = 0x7FFFFFFF - 255;
+    return M < 0 || M > most || K < 16 || K % 16 || K > most || N < 16 || N % 16 || N > most;
+}
 
 // Rows of a TMA box of activations: what a tile can have.
 int fp8_box(int S) { return S >= 128 ? 128 : (S + 7) / 8 * 8; }

@@ -899,8 +899,8 @@ size_t qg_workspace_size(qg_op op, int M, int K, int N)
         if (M < 1 || K < 8 || K % 8 || K > 16384 || N < 1) return 0;
         return std::max(gptq_carve(nullptr, K, N).bytes, gptq_blocked_carve(nullptr, M, K, N).bytes);
     }
-    if (op == QG_OP_GEMM_FP8) return M < 1 || fp8_bad_shape(K, N) ? 0 : fp8_workspace(M, K, false);
-    if (op == QG_OP_GEMM_FP8_EXPERTS) return M < 1 || fp8_bad_shape(K, N) ? 0 : fp8_workspace(M, K, true);
+    if (op == QG_OP_GEMM_FP8) return M < 1 || fp8_bad_shape(M, K, N) ? 0 : fp8_workspace(M, K, false);
+    if (op == QG_OP_GEMM_FP8_EXPERTS) return M < 1 || fp8_bad_shape(M, K, N) ? 0 : fp8_workspace(M, K, true);
     if (op == QG_OP_EXPERT_SLOTS) return M < 1 || slots_bad_shape(M, K, N) ? 0 : slots_workspace(M, K, N);
     if (M < 1 || K < 128 || N < 8 || K % 128) return 0;
     switch (op) {
@@ -1547,7 +1547,7 @@ qg_status qg_quantize_weight_fp8(const void* W, qg_dtype wdt, int E, int K, int 
                                  qg_stream_t stream)
 {
     if (wdt != QG_F16 && wdt != QG_BF16 && wdt != QG_F32) return QG_ERR_DTYPE;
-    if (E < 1 || fp8_bad_shape(K, N) || E > 65535 || (K + 127) / 128 > 65535) return QG_ERR_SHAPE;
+    if (E < 1 || fp8_bad_shape(0, K, N) || E > 65535 || (K + 127) / 128 > 65535) return QG_ERR_SHAPE;
     if (!W || !Wq || !ws) return QG_ERR_NULL;
     if (misaligned(W) || misaligned(Wq) || misaligned(ws)) return QG_ERR_ALIGN;
     return wdt == QG_F32    ? quantize_weight_fp8<qg::IN_F32>(W, E, K, N, Wq, ws, stream)
@@ -1559,7 +1559,7 @@ qg_status qg_gemm_fp8(const uint8_t* Xq, const float* xs, int M, int K, const ui
                       void* Y, qg_dtype ydt, void* workspace, size_t ws_bytes, qg_stream_t stream)
 {
     if (ydt != QG_F16 && ydt != QG_BF16) return QG_ERR_DTYPE;
-    if (M < 0 || fp8_bad_shape(K, N)) return QG_ERR_SHAPE;
+    if (fp8_bad_shape(M, K, N)) return QG_ERR_SHAPE;
     if (M == 0) return QG_OK;
     return fp8_gemm(Xq, xs, M, K, nullptr, nullptr, M, 1, Wq, ws, N, Y, ydt, workspace, ws_bytes, stream);
 }
@@ -1569,7 +1569,8 @@ qg_status qg_gemm_fp8_experts(const uint8_t* Xq, const float* xs, int Mx, int K,
                               qg_dtype ydt, void* workspace, size_t ws_bytes, qg_stream_t stream)
 {
     if (ydt != QG_F16 && ydt != QG_BF16) return QG_ERR_DTYPE;
-    if (S < 0 || Mx < 0 || fp8_bad_shape(K, N) || E < 1 || E > qg::kMaxExperts) return QG_ERR_SHAPE;
+    if (fp8_bad_shape(S, K, N) || Mx < 0 || E < 1 || E > qg::kMaxExperts) return QG_ERR_SHAPE;
+    if (slot_token && K > 65535 * 4096) return QG_ERR_SHAPE;   // the gather's grid
     if (S == 0) return QG_OK;
     if (Mx < 1 || (!slot_token && Mx < S)) return QG_ERR_SHAPE;
     if (!offsets) return QG_ERR_NULL;
@@ -1582,9 +1583,9 @@ qg_status qg_route_topk(const void* logits, qg_dtype ldt, int M, int E, const fl
 {
     if ((ldt != QG_F16 && ldt != QG_BF16 && ldt != QG_F32) || (score != QG_SCORE_SOFTMAX && score != QG_SCORE_SIGMOID))
         return QG_ERR_DTYPE;
-    if (M < 0 || E < 1 || E > qg::kMaxExperts || topk < 1 || topk > std::min(E, qg::kMaxTopk) || n_group < 1 ||
-        n_group > qg::kMaxExpertGroups || E % n_group || topk_group < 1 || topk_group > n_group || group_top < 1 ||
-        group_top > 2 || topk > topk_group * (E / n_group))
+    if (M < 0 || M > 0x7FFFFFFF - 3 || E < 1 || E > qg::kMaxExperts || topk < 1 ||
+        topk > std::min(E, qg::kMaxTopk) || n_group < 1 || n_group > qg::kMaxExpertGroups || E % n_group ||
+        topk_group < 1 || topk_group > n_group || group_top < 1 || group_top > 2 || topk > topk_group * (E / n_group))
         return QG_ERR_SHAPE;
     if (M == 0) return QG_OK;
     if (!logits || !idx || !weights) return QG_ERR_NULL;

@@ -455,7 +455,7 @@ qg_status qg_awq_search(const uint16_t* Xcal, int Mc, int K, const float* W, int
  *   ws fp32 [E][G][NB].
  * A group with a NaN or an infinity gets the scale NaN and codes 0 (its products are NaN,
  *   as the unquantized ones would be) and sets QG_ERR_NONFINITE.
- * Rules: K % 16 == 0; weights: N % 16 == 0, E >= 1 (K / 128 and E below 65536).
+ * Rules: K % 16 == 0; weights: N % 16 == 0, N < 2^31 - 255, E >= 1 (K / 128 and E below 65536).
  * ------------------------------------------------------------------------ */
 qg_status qg_quantize_act_fp8(const void* X, qg_dtype xdt, int M, int K, uint8_t* Xq, float* xs,
                               qg_stream_t stream);
@@ -473,7 +473,7 @@ qg_status qg_quantize_weight_fp8(const void* W, qg_dtype wdt, int E, int K, int 
  * NaN codes and scales give NaN in the rows and columns that read them, and there only.
  * Everything the call reads, weights and scales among it, may be written by the kernel right
  *   before it in the same stream, whether that lets its dependents start early or not.
- * Rules: K % 16 == 0, N % 16 == 0.
+ * Rules: K % 16 == 0, N % 16 == 0; M, K and N below 2^31 - 255.
  * workspace: required when qg_workspace_size(QG_OP_GEMM_FP8, M, K, N) is not 0, and then
  *   at least that many bytes (NULL -> QG_ERR_NULL, smaller -> QG_ERR_WORKSPACE); contents
  *   irrelevant.  Calls that may run concurrently need workspaces of their own.
@@ -500,7 +500,7 @@ qg_status qg_gemm_fp8(const uint8_t* Xq, const float* xs, int M, int K, const ui
  *   with a NaN or +inf logit or key goes to no expert and sets QG_ERR_NONFINITE.
  * logits fp16, bf16 or fp32 [M][E] (ldt); bias fp32 [E] or NULL; idx int32 [M][topk];
  * weights fp32 [M][topk].
- * Rules: 1 <= E <= 512, 1 <= topk <= min(32, E), 1 <= n_group <= 32, E % n_group == 0,
+ * Rules: M < 2^31 - 3, 1 <= E <= 512, 1 <= topk <= min(32, E), 1 <= n_group <= 32, E % n_group == 0,
  *   1 <= topk_group <= n_group, group_top 1 or 2, topk <= topk_group * (E / n_group).
  * ------------------------------------------------------------------------ */
 qg_status qg_route_topk(const void* logits, qg_dtype ldt, int M, int E, const float* bias,
@@ -528,7 +528,8 @@ qg_status qg_expert_slots(const int32_t* idx, int M, int topk, int E, int32_t* o
  * [E][G][NB]; Y fp16 or bf16 [S][N].
  * Device error: QG_ERR_RANGE -- offsets that are not ascending within 0 .. S (nothing is
  *   computed), or a slot_token outside 0 .. Mx - 1 (its row counts as 0).
- * Rules: K % 16 == 0, N % 16 == 0, 1 <= E <= 512; S == 0 returns QG_OK.
+ * Rules: K % 16 == 0, N % 16 == 0, 1 <= E <= 512; S, K and N below 2^31 - 255 (with slot_token K
+ *   at most 65535 * 4096); S == 0 returns QG_OK.
  * workspace: as for qg_gemm_fp8, of qg_workspace_size(QG_OP_GEMM_FP8_EXPERTS, S, K, N). */
 qg_status qg_gemm_fp8_experts(const uint8_t* Xq, const float* xs, int Mx, int K,
                               const int32_t* slot_token, const int32_t* offsets, int S, int E,
