@@ -225,8 +225,8 @@ QG_DEV_INLINE void fp8_fold(float (&acc)[CW], uint32_t addr, float sc, F release
 // ---------------------------------------------------------------------------
 // Splitting costs the join: about 11 us for a few rows and 20 us for 128, where a step of 128
 // columns takes 0.32 us (256: 0.6), so the longest CTA has to save fp8_min_saved() steps of 128
-// columns.  K = 11008, N = 4096, 4 rows (86 steps down to 19): 27.5 -> 17.1 us; K = 4096 (32 down
-// to 7): 11.8 -> 13.8 us, left whole; K = 11008 with 128 rows: no difference.
+// columns.  K = 11008, N = 4096, 4 rows (86 steps down to 19): 27.5 us whole, 18.5 split; K = 4096
+// (32 down to 7): 11.8 and 13.8 us, left whole; K = 11008 with 128 rows: no difference.
 constexpr int kFp8MinUnits = 4;   // of a piece
 __host__ __device__ inline int fp8_min_saved(int rows) { return 34 + rows / 4; }
 
@@ -352,9 +352,9 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const Fp8Params p, const 
 // 4..11 fold: thread = row, BN / 2 columns, whose weight scale is one number, so a step costs a
 // thread one scale (which it loads itself, four groups ahead) and BN / 2 fma.
 //
-// Measured: 8192 x 8192 x 28672 2.0 ms (1.9 PFLOP/s; the fold bounds it, and the power cap);
-// 4096 x 4096 x 4096 78..93 us; 1 x 4096 x 12288 13.3 us (3.8 TB/s), 16 x 8192 x 28672 42 us
-// (5.6 TB/s).
+// Measured in a graph: 8192 x 8192 x 28672 2.0..2.15 ms (1.8..1.9 PFLOP/s; the fold bounds it, and the
+// power cap: 2.2..2.3 ms on normal data); 4096 x 4096 x 4096 74..84 us; 1 x 4096 x 12288 13.6 us
+// (3.7 TB/s), 16 x 8192 x 28672 41..44 us (5.3..5.7 TB/s).
 // Few rows: the tensor core then multiplies rows that go nowhere, but a step's weights (16 or
 // 32 KB) take HBM as long as a step takes the tensor core; with operands swapped and a narrow N
 // it was no faster.  Mapped rows are gathered by

@@ -113,9 +113,10 @@ __global__ void __launch_bounds__(256) quantize_act_fp8_kernel(const uint16_t* _
 
 // Weights [E][K][N] (fp32, bf16 or fp16), N % 16 == 0: one CTA per block of 128 x 128, held
 // in registers between the maximum and the codes.  Thread (q, r) has columns 4q .. 4q+3 of
-// rows r, r + 16, ..: a warp reads and writes whole row segments.  4096 x 12288 fp32: 57 us,
-// 4.4 TB/s (two CTAs fit an SM, and their load and store phases leave HBM idle in between; three,
-// with spills, were no faster; a checked three-instruction quotient for fp32 slower, 64 us).
+// rows r, r + 16, ..: a warp reads and writes whole row segments.  4096 x 12288: fp32 60 us, 4.2
+// TB/s, bf16 54 us, 2.8 TB/s (two CTAs fit an SM, and their load and store phases leave HBM idle in
+// between; three, with spills, were no faster; a checked three-instruction quotient for fp32
+// slower, 64 us).
 template <int T>
 __global__ void __launch_bounds__(512) quantize_weight_fp8_kernel(const void* __restrict__ W, int K, int N,
                                                                   uint8_t* __restrict__ Wq, float* __restrict__ ws)
